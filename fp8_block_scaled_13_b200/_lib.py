@@ -24,6 +24,11 @@ PURO_ERR_DEVICE_TIMEOUT = -7
 PURO_ROWWISE = 1
 PURO_COLWISE = 2
 PURO_BOTH = 3
+PURO_BF16 = 4
+PURO_GATE_NONE = 0
+PURO_GATE_TOKEN = 1
+PURO_GATE_CHANNEL = 2
+PURO_GATE_FULL = 3
 PURO_DW_BF16 = 0
 PURO_DW_F32 = 1
 PURO_DW_F32_ACCUMULATE = 2
@@ -38,6 +43,11 @@ EXPORTS = (
     "puro_fp8_gemm_wgrad",
     "puro_fp8_gemm_wgrad_f32",
     "puro_fp8_gemm_dgrad_wgrad",
+    "puro_fp8_residual_norm",
+    "puro_fp8_residual_norm_workspace_bytes",
+    "puro_fp8_residual_norm_backward",
+    "puro_fp8_swiglu",
+    "puro_fp8_swiglu_backward",
     "puro_fp8_device_status",
     "puro_fp8_status_string",
     "puro_fp8_test_bounded_wait",
@@ -75,6 +85,15 @@ def load() -> ctypes.CDLL:
     lib.puro_fp8_gemm_wgrad_f32.argtypes = [P, I, P, P, I, P, P, I, I, I, I, INT, P]
     lib.puro_fp8_gemm_dgrad_wgrad.argtypes = [P, I, P, P, I, P, P, I, P, I, P, P, I, P, P, I,
                                               I, I, I, INT, P]
+    F = ctypes.c_float
+    codes = [INT, P, I, P, P, I, P, P, I]  # layout, q, ld_q, s, qt, ld_qt, st, bf16, ld_bf16
+    lib.puro_fp8_residual_norm.argtypes = [P, I, P, I, P, P, INT, P, I, INT, INT, F, F, I, I, P, I, P, P, *codes, P]
+    lib.puro_fp8_residual_norm_workspace_bytes.argtypes = [I, I]
+    lib.puro_fp8_residual_norm_workspace_bytes.restype = I
+    lib.puro_fp8_residual_norm_backward.argtypes = [P, I, P, I, P, I, P, P, I, P, P, P, INT, P, I, INT, INT, F, I, I,
+                                                    P, I, P, P, P, I, INT, *codes, P, P]
+    lib.puro_fp8_swiglu.argtypes = [P, I, I, I, *codes, P]
+    lib.puro_fp8_swiglu_backward.argtypes = [P, I, P, I, I, I, *codes, P]
     lib.puro_fp8_device_status.argtypes = [P]
     lib.puro_fp8_status_string.argtypes = [INT]
     lib.puro_fp8_status_string.restype = ctypes.c_char_p
@@ -82,7 +101,7 @@ def load() -> ctypes.CDLL:
     I32 = ctypes.c_int32
     lib.puro_fp8_test_schedule.argtypes = [I32, I32, I32, I32, I32, P, P]
     for name in EXPORTS:
-        if name not in ("puro_fp8_status_string", "puro_fp8_blocked_scale_bytes"):
+        if name != "puro_fp8_status_string" and not name.endswith("_bytes"):
             getattr(lib, name).restype = INT
     _lib = lib
     return lib
@@ -131,6 +150,26 @@ def puro_fp8_gemm_dgrad_wgrad(qdy, ld_qdy, sdy, qwt, ld_qwt, sw_bwd, dx, ld_dx, 
     return load().puro_fp8_gemm_dgrad_wgrad(qdy, ld_qdy, sdy, qwt, ld_qwt, sw_bwd, dx, ld_dx, qdyt,
                                             ld_qdyt, sdyt, qxt, ld_qxt, sxt, dw, ld_dw, m, n, k,
                                             dw_kind, stream)
+
+
+def puro_fp8_residual_norm(*args) -> int:
+    return load().puro_fp8_residual_norm(*args)
+
+
+def puro_fp8_residual_norm_workspace_bytes(rows, cols) -> int:
+    return load().puro_fp8_residual_norm_workspace_bytes(rows, cols)
+
+
+def puro_fp8_residual_norm_backward(*args) -> int:
+    return load().puro_fp8_residual_norm_backward(*args)
+
+
+def puro_fp8_swiglu(*args) -> int:
+    return load().puro_fp8_swiglu(*args)
+
+
+def puro_fp8_swiglu_backward(*args) -> int:
+    return load().puro_fp8_swiglu_backward(*args)
 
 
 def puro_fp8_device_status(stream) -> int:

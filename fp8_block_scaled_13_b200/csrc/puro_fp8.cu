@@ -20,7 +20,9 @@
 
 #include "../../include/puro_fp8.h"
 #include "common.cuh"
+#include "gated.cuh"
 #include "gemm.cuh"
+#include "norm.cuh"
 #include "quant.cuh"
 
 namespace {
@@ -117,6 +119,23 @@ int make_map_scales(CUtensorMap* m, const void* base, int64_t rows, int64_t grou
   return r == CUDA_SUCCESS ? PURO_OK : PURO_ERR_CUDA;
 }
 
+// The transposed codes qt [cols][ld_qt] as a 3-D tensor {qt_cols, cols/8,
+// 8} with strides {1, 8 ld_qt, ld_qt} bytes and 128-byte swizzle: a 128 x
+// 16 x 8 box is one tile, its transposed row 8 c_hi + c_lo at staging row
+// 16 c_lo + c_hi, which is how the kernels stage it.  qt_cols: the bytes of
+// a transposed row that are written (rows rounded up to 16 for
+// activations, whose padding codes are 0; n for weights).
+int make_map_qt(CUtensorMap* m, void* qt, int64_t qt_cols, int64_t cols, int64_t ld_qt) {
+  cuuint64_t dims[3] = {(cuuint64_t)qt_cols, (cuuint64_t)(cols / 8), 8};
+  cuuint64_t strides[2] = {(cuuint64_t)ld_qt * 8, (cuuint64_t)ld_qt};
+  cuuint32_t box[3] = {128, 16, 8};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, qt, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PURO_OK : PURO_ERR_CUDA;
+}
+
 int64_t g4_of(int64_t groups) { return (groups + 3) / 4; }
 
 int launch_status() {
@@ -140,23 +159,10 @@ int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, co
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return PURO_ERR_CUDA;
-  // The transposed codes qt [cols][ld_qt] as a 3-D tensor {qt_cols, cols/8,
-  // 8} with strides {1, 8 ld_qt, ld_qt} bytes and 128-byte swizzle: a 128 x
-  // 16 x 8 box is one tile, its transposed row 8 c_hi + c_lo at staging row
-  // 16 c_lo + c_hi, which is how the kernel stages it.  qt_cols: the bytes of
-  // a transposed row that are written (rows rounded up to 16 for
-  // activations, whose padding codes are 0; n for weights).
   CUtensorMap mqt = m;
   if (COL) {
-    const int64_t qt_cols = BLOCK ? p.rows : (p.rows + 15) / 16 * 16;
-    cuuint64_t qdims[3] = {(cuuint64_t)qt_cols, (cuuint64_t)(p.cols / 8), 8};
-    cuuint64_t qstrides[2] = {(cuuint64_t)p.ld_qt * 8, (cuuint64_t)p.ld_qt};
-    cuuint32_t qbox[3] = {128, 16, 8};
-    cuuint32_t qestr[3] = {1, 1, 1};
-    if (g_encode(&mqt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.qt, qdims, qstrides, qbox, qestr,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return PURO_ERR_CUDA;
+    if ((st = make_map_qt(&mqt, p.qt, BLOCK ? p.rows : (p.rows + 15) / 16 * 16, p.cols, p.ld_qt)) != PURO_OK)
+      return st;
   }
   auto kern = puro::quant_kernel<ROW, COL, BLOCK, RSHFL, STAGES>;
   constexpr uint32_t smem = puro::quant_smem_bytes<STAGES>();
@@ -761,3 +767,358 @@ extern "C" int puro_fp8_quant_act_static_scratch(const void* x, int64_t rows, in
     return PURO_ERR_CUDA;
   return puro_fp8_quant_act(x, rows, cols, ld_x, layout, q, ld_q, s, qt, ld_qt, st, ctr, stream);
 }
+
+// ---------------------------------------------------------------- norms and gated activation
+
+namespace {
+
+// Checks the outputs of a kernel that leaves a BF16 result [rows, cols] as
+// codes or as it is, and fills in where they go.
+int code_out_args(int layout, int64_t rows, int64_t cols, void* q, int64_t ld_q, void* s, void* qt,
+                  int64_t ld_qt, void* st, void* bf, int64_t ld_bf, puro::CodeOut* o) {
+  *o = puro::CodeOut{};
+  int r;
+  if (layout == PURO_BF16) {
+    if ((r = check_mat(bf, ld_bf, cols, 2)) != PURO_OK) return r;
+    o->bf = static_cast<__nv_bfloat16*>(bf);
+    o->ld_bf = ld_bf;
+    return PURO_OK;
+  }
+  if (layout & PURO_ROWWISE) {
+    if ((r = check_mat(q, ld_q, cols, 1)) != PURO_OK) return r;
+    if (!s) return PURO_ERR_NULL;
+    if (!aligned16(s)) return PURO_ERR_ALIGN;
+    o->q = static_cast<uint8_t*>(q);
+    o->ld_q = ld_q;
+    o->s = static_cast<uint8_t*>(s);
+    o->s_g4 = g4_of(cols / 128);
+  }
+  if (layout & PURO_COLWISE) {
+    if ((r = check_mat(qt, ld_qt, (rows + 15) / 16 * 16, 1)) != PURO_OK) return r;
+    if (!st) return PURO_ERR_NULL;
+    if (!aligned16(st)) return PURO_ERR_ALIGN;
+    o->qt = static_cast<uint8_t*>(qt);
+    o->ld_qt = ld_qt;
+    o->st = static_cast<uint8_t*>(st);
+    o->st_g4 = g4_of((rows + 127) / 128);
+  }
+  return PURO_OK;
+}
+
+bool known_layout(int layout) {
+  return layout == PURO_ROWWISE || layout == PURO_COLWISE || layout == PURO_BOTH || layout == PURO_BF16;
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Sizes and parameters that both directions of the norms take.
+int norm_common_args(const void* w_pre, const void* w_post, int w_f32, const void* gate, int64_t ld_gate,
+                     int gate_kind, int gate_f32, float scale, const void* h, int64_t rows, int64_t cols,
+                     puro::NormParams* p) {
+  if (!w_pre) return PURO_ERR_NULL;
+  const uintptr_t wa = w_f32 ? 4 : 2;
+  if (!aligned_to(w_pre, wa) || !aligned_to(w_post, wa)) return PURO_ERR_ALIGN;
+  if (gate_kind != PURO_GATE_NONE) {
+    if (!gate) return PURO_ERR_NULL;
+    if (gate_kind == PURO_GATE_FULL) {
+      int r;
+      if ((r = check_mat(gate, ld_gate, cols, 2)) != PURO_OK) return r;
+    } else if (!aligned_to(gate, gate_f32 ? 4 : 2)) {
+      return PURO_ERR_ALIGN;
+    }
+  }
+  p->rows = rows;
+  p->cols = (int32_t)cols;
+  p->w_pre = w_pre;
+  p->w_post = h ? w_post : nullptr;
+  p->w_f32 = w_f32;
+  p->gate = h ? gate : nullptr;
+  p->ld_gate = ld_gate;
+  p->gate_kind = h ? gate_kind : PURO_GATE_NONE;
+  p->gate_f32 = gate_f32;
+  p->scale = scale;
+  return PURO_OK;
+}
+
+int norm_flags(int w_f32, int gate_kind, int gate_f32, int64_t rows, int64_t cols, int layout) {
+  if (!known_layout(layout)) return PURO_ERR_LAYOUT;
+  if (gate_kind < PURO_GATE_NONE || gate_kind > PURO_GATE_FULL || (w_f32 & ~1) || (gate_f32 & ~1) ||
+      (gate_kind == PURO_GATE_FULL && gate_f32))
+    return PURO_ERR_LAYOUT;
+  if (rows < 0 || cols < 0 || rows >= kMaxDim || cols % 128 || cols > puro::kNormMaxCols) return PURO_ERR_SHAPE;
+  return PURO_OK;
+}
+
+// Launches `kern` on `grid` CTAs in clusters of `cluster` (1: none).
+template <class Kern>
+int launch_norm_cfg(Kern kern, const puro::NormParams& p, int64_t grid, int threads, uint32_t smem, int cluster,
+                    std::atomic<bool>* attr_done, const DeviceInfo& dev, cudaStream_t stream) {
+  if (!attr_done[dev.index].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return PURO_ERR_CUDA;
+    attr_done[dev.index].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PURO_ERR_CUDA;
+  }
+  return PURO_OK;
+}
+
+template <int MAXT, int RPC, bool COL>
+int launch_norm(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevices] = {};
+  const int threads = (p.cols / 8 + 31) / 32 * 32;
+  // Without transposed codes no cluster is needed, and a CTA takes as many
+  // rows (a power of two, so that CTAs never straddle a 128-row block of
+  // scales) as still leave every SM two CTAs.
+  p.rpc = RPC;
+  if (!COL)
+    while (p.rpc > 1 && p.rows < (int64_t)p.rpc * 2 * dev.sms) p.rpc /= 2;
+  const int64_t grid = COL ? (p.rows + 127) / 128 * (128 / RPC) : (p.rows + p.rpc - 1) / p.rpc;
+  return launch_norm_cfg(puro::norm_kernel<MAXT, RPC, COL>, p, grid, threads,
+                         puro::norm_smem_bytes<RPC, COL, false>(p.cols), COL ? 128 / RPC : 1, done, dev, stream);
+}
+
+template <int MAXT, int RPC, bool COL>
+int launch_norm_backward(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevices] = {};
+  const int threads = (p.cols / 8 + 31) / 32 * 32;
+  p.rpc = RPC;
+  return launch_norm_cfg(puro::norm_backward_kernel<MAXT, RPC, COL>, p, (p.rows + 127) / 128 * (128 / RPC),
+                         threads, puro::norm_smem_bytes<RPC, COL, true>(p.cols), 128 / RPC, done, dev, stream);
+}
+
+template <bool BWD, bool ROW, bool COL, bool BF>
+int launch_gated_cfg(const puro::GatedParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap m;
+  memset(&m, 0, sizeof(m));
+  if (COL) {
+    int st;
+    if ((st = get_encoder()) != PURO_OK) return st;
+    if ((st = make_map_qt(&m, p.out.qt, (p.rows + 15) / 16 * 16, (BWD ? 2 : 1) * (int64_t)p.f, p.out.ld_qt)) !=
+        PURO_OK)
+      return st;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((p.rows + 127) / 128 * p.tiles_c));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = COL ? puro::kGatedSmemBytes : 0;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, puro::gated_kernel<BWD, ROW, COL, BF>, m, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PURO_ERR_CUDA;
+  }
+  return PURO_OK;
+}
+
+template <bool BWD>
+int gated(const void* da, int64_t ld_da, const void* gu, int64_t ld_gu, int64_t rows, int64_t f, int layout,
+          void* q, int64_t ld_q, void* s, void* qt, int64_t ld_qt, void* st, void* bf, int64_t ld_bf,
+          void* stream) {
+  if (!known_layout(layout)) return PURO_ERR_LAYOUT;
+  if (rows < 0 || f < 0 || rows >= kMaxDim || f >= kMaxDim / 2 || f % 128) return PURO_ERR_SHAPE;
+  if (rows == 0 || f == 0) return PURO_OK;
+  if ((f / 128) * ((rows + 127) / 128) >= kMaxDim / 2) return PURO_ERR_SHAPE;
+  int r;
+  if ((r = check_mat(gu, ld_gu, 2 * f, 2)) != PURO_OK) return r;
+  if (BWD && (r = check_mat(da, ld_da, f, 2)) != PURO_OK) return r;
+  puro::GatedParams p{};
+  if ((r = code_out_args(layout, rows, (BWD ? 2 : 1) * f, q, ld_q, s, qt, ld_qt, st, bf, ld_bf, &p.out)) != PURO_OK)
+    return r;
+  DeviceInfo* dev = nullptr;
+  if ((r = current_device(&dev)) != PURO_OK) return r;
+  p.rows = rows;
+  p.f = (int32_t)f;
+  p.tiles_c = (int32_t)(f / 128);
+  p.gu = static_cast<const __nv_bfloat16*>(gu);
+  p.ld_gu = ld_gu;
+  p.da = static_cast<const __nv_bfloat16*>(da);
+  p.ld_da = ld_da;
+  cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  switch (layout) {
+    case PURO_ROWWISE: return launch_gated_cfg<BWD, true, false, false>(p, *dev, sm);
+    case PURO_COLWISE: return launch_gated_cfg<BWD, false, true, false>(p, *dev, sm);
+    case PURO_BOTH: return launch_gated_cfg<BWD, true, true, false>(p, *dev, sm);
+    default: return launch_gated_cfg<BWD, false, false, true>(p, *dev, sm);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t ld_h, const void* w_pre,
+                           const void* w_post, int w_f32, const void* gate, int64_t ld_gate, int gate_kind,
+                           int gate_f32, float scale, float eps, int64_t rows, int64_t cols, void* y, int64_t ld_y,
+                           float* rstd, float* rstd_post, int layout, void* q, int64_t ld_q, void* s, void* qt,
+                           int64_t ld_qt, void* st, void* n, int64_t ld_n, void* stream) {
+  int r;
+  if ((r = norm_flags(w_f32, gate_kind, gate_f32, rows, cols, layout)) != PURO_OK) return r;
+  if (!(eps > 0.f)) return PURO_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return PURO_OK;
+  puro::NormParams p{};
+  if ((r = check_mat(x, ld_x, cols, 2)) != PURO_OK) return r;
+  if (h) {
+    if ((r = check_mat(h, ld_h, cols, 2)) != PURO_OK) return r;
+    if ((r = check_mat(y, ld_y, cols, 2)) != PURO_OK) return r;
+  }
+  if ((r = norm_common_args(w_pre, w_post, w_f32, gate, ld_gate, gate_kind, gate_f32, scale, h, rows, cols, &p)) !=
+      PURO_OK)
+    return r;
+  if (!rstd || (p.w_post && !rstd_post)) return PURO_ERR_NULL;
+  if (!aligned_to(rstd, 4) || !aligned_to(rstd_post, 4)) return PURO_ERR_ALIGN;
+  if ((r = code_out_args(layout, rows, cols, q, ld_q, s, qt, ld_qt, st, n, ld_n, &p.out)) != PURO_OK) return r;
+  DeviceInfo* dev = nullptr;
+  if ((r = current_device(&dev)) != PURO_OK) return r;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.ld_x = ld_x;
+  p.h = static_cast<const __nv_bfloat16*>(h);
+  p.ld_h = ld_h;
+  p.eps = eps;
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.ld_y = ld_y;
+  p.rstd = rstd;
+  p.rstd_post = rstd_post;
+  cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  const bool col = p.out.qt != nullptr;
+  if (cols <= 2048) return col ? launch_norm<256, 16, true>(p, *dev, sm) : launch_norm<256, 16, false>(p, *dev, sm);
+  if (cols <= 4096) return col ? launch_norm<512, 16, true>(p, *dev, sm) : launch_norm<512, 16, false>(p, *dev, sm);
+  return col ? launch_norm<1024, 8, true>(p, *dev, sm) : launch_norm<1024, 8, false>(p, *dev, sm);
+}
+
+int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return (rows + 127) / 128 * 2 * cols * (int64_t)sizeof(float);
+}
+
+int puro_fp8_residual_norm_backward(const void* dn, int64_t ld_dn, const void* dy, int64_t ld_dy, const void* y,
+                                    int64_t ld_y, const float* rstd, const void* h, int64_t ld_h,
+                                    const float* rstd_post, const void* w_pre, const void* w_post, int w_f32,
+                                    const void* gate, int64_t ld_gate, int gate_kind, int gate_f32, float scale,
+                                    int64_t rows, int64_t cols, void* dx, int64_t ld_dx, float* dw_pre,
+                                    float* dw_post, void* dgate, int64_t ld_dgate, int accumulate, int layout,
+                                    void* q, int64_t ld_q, void* s, void* qt, int64_t ld_qt, void* st, void* dh,
+                                    int64_t ld_dh, void* workspace, void* stream) {
+  int r;
+  if ((r = norm_flags(w_f32, gate_kind, gate_f32, rows, cols, layout)) != PURO_OK) return r;
+  if (accumulate != 0 && accumulate != 1) return PURO_ERR_LAYOUT;
+  if (cols == 0) return PURO_OK;
+  puro::NormParams p{};
+  if ((r = norm_common_args(w_pre, w_post, w_f32, gate, ld_gate, rows ? gate_kind : PURO_GATE_NONE, gate_f32, scale,
+                            h, rows, cols, &p)) != PURO_OK)
+    return r;
+  // (an empty h has no address: without rows, the weights and the gate alone
+  // say which gradients there are)
+  if (rows == 0) p.w_post = w_post;
+  const bool channel = (h || rows == 0) && gate_kind == PURO_GATE_CHANNEL;
+  if (!dw_pre || (p.w_post && !dw_post) || (channel && (!dgate || !gate))) return PURO_ERR_NULL;
+  if (!aligned_to(dw_pre, 4) || !aligned_to(dw_post, 4) || (channel && !aligned_to(dgate, 4))) return PURO_ERR_ALIGN;
+  if (rows > 0) {
+    if ((r = check_mat(dn, ld_dn, cols, 2)) != PURO_OK) return r;
+    if (dy && (r = check_mat(dy, ld_dy, cols, 2)) != PURO_OK) return r;
+    if ((r = check_mat(y, ld_y, cols, 2)) != PURO_OK) return r;
+    if ((r = check_mat(dx, ld_dx, cols, 2)) != PURO_OK) return r;
+    if (!rstd || !workspace) return PURO_ERR_NULL;
+    if (!aligned_to(rstd, 4) || !aligned16(workspace)) return PURO_ERR_ALIGN;
+    if (h) {
+      if ((r = check_mat(h, ld_h, cols, 2)) != PURO_OK) return r;
+      if (p.w_post && !rstd_post) return PURO_ERR_NULL;
+      if (!aligned_to(rstd_post, 4)) return PURO_ERR_ALIGN;
+      if (p.gate_kind == PURO_GATE_FULL && (r = check_mat(dgate, ld_dgate, cols, 2)) != PURO_OK) return r;
+      if (p.gate_kind == PURO_GATE_TOKEN) {
+        if (!dgate) return PURO_ERR_NULL;
+        if (!aligned_to(dgate, 4)) return PURO_ERR_ALIGN;
+      }
+      if ((r = code_out_args(layout, rows, cols, q, ld_q, s, qt, ld_qt, st, dh, ld_dh, &p.out)) != PURO_OK) return r;
+    }
+  }
+  DeviceInfo* dev = nullptr;
+  if ((r = current_device(&dev)) != PURO_OK) return r;
+  cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  if (rows > 0) {
+    p.dn = static_cast<const __nv_bfloat16*>(dn);
+    p.ld_dn = ld_dn;
+    p.dy = static_cast<const __nv_bfloat16*>(dy);
+    p.ld_dy = ld_dy;
+    p.x = static_cast<const __nv_bfloat16*>(y);
+    p.ld_x = ld_y;
+    p.h = static_cast<const __nv_bfloat16*>(h);
+    p.ld_h = ld_h;
+    p.rstd = const_cast<float*>(rstd);
+    p.rstd_post = const_cast<float*>(rstd_post);
+    p.dx = static_cast<__nv_bfloat16*>(dx);
+    p.ld_dx = ld_dx;
+    p.dgate = dgate;
+    p.ld_dgate = ld_dgate;
+    p.part = static_cast<float*>(workspace);
+    const bool col = p.out.qt != nullptr;
+    if (cols <= 2048)
+      r = col ? launch_norm_backward<256, 16, true>(p, *dev, sm) : launch_norm_backward<256, 16, false>(p, *dev, sm);
+    else if (cols <= 4096)
+      r = col ? launch_norm_backward<512, 16, true>(p, *dev, sm) : launch_norm_backward<512, 16, false>(p, *dev, sm);
+    else
+      r = col ? launch_norm_backward<1024, 8, true>(p, *dev, sm) : launch_norm_backward<1024, 8, false>(p, *dev, sm);
+    if (r != PURO_OK) return r;
+  }
+  puro::NormColumnParams c{};
+  c.part = static_cast<const float*>(workspace);
+  c.parts = (rows + 127) / 128;
+  c.cols = (int32_t)cols;
+  c.w_post = p.w_post;
+  c.gate = channel ? gate : nullptr;
+  c.w_f32 = w_f32;
+  c.gate_f32 = gate_f32;
+  c.scale = scale;
+  c.accumulate = accumulate;
+  c.dw_pre = dw_pre;
+  c.dw_post = p.w_post ? dw_post : nullptr;
+  c.dgate = channel ? static_cast<float*>(dgate) : nullptr;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(cols / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = sm;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, puro::norm_column_kernel, c) != cudaSuccess) {
+    cudaGetLastError();
+    return PURO_ERR_CUDA;
+  }
+  return PURO_OK;
+}
+
+int puro_fp8_swiglu(const void* gu, int64_t ld_gu, int64_t rows, int64_t f, int layout, void* q, int64_t ld_q,
+                    void* s, void* qt, int64_t ld_qt, void* st, void* a, int64_t ld_a, void* stream) {
+  return gated<false>(nullptr, 0, gu, ld_gu, rows, f, layout, q, ld_q, s, qt, ld_qt, st, a, ld_a, stream);
+}
+
+int puro_fp8_swiglu_backward(const void* da, int64_t ld_da, const void* gu, int64_t ld_gu, int64_t rows, int64_t f,
+                             int layout, void* q, int64_t ld_q, void* s, void* qt, int64_t ld_qt, void* st,
+                             void* dgu, int64_t ld_dgu, void* stream) {
+  return gated<true>(da, ld_da, gu, ld_gu, rows, f, layout, q, ld_q, s, qt, ld_qt, st, dgu, ld_dgu, stream);
+}
+
+}  // extern "C"

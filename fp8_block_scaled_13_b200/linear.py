@@ -381,9 +381,10 @@ def device_status() -> int:
     return _lib.puro_fp8_device_status(_stream())
 
 
-def linear_forward(x: torch.Tensor, w: torch.Tensor | None = None, wq: QuantWeight | None = None):
+def linear_forward(x: torch.Tensor | QuantAct, w: torch.Tensor | None = None, wq: QuantWeight | None = None):
     """Quantize X (and W, unless its quantization `wq` is passed in), then
-    Y = X W^T.  Returns (y, xq, wq).
+    Y = X W^T.  Returns (y, xq, wq).  X may be a QuantAct already, e.g. from
+    residual_norm or swiglu.
 
     Passing the previous call's `wq` skips re-quantizing a weight that has not
     changed, e.g. across the micro-batches of one gradient-accumulation step
@@ -392,17 +393,19 @@ def linear_forward(x: torch.Tensor, w: torch.Tensor | None = None, wq: QuantWeig
         if w is None:
             raise ValueError("pass the weight or its quantization")
         wq = quant_weight(w, transpose=True)
-    xq = quant_act(x, "both")
+    xq = x if isinstance(x, QuantAct) else quant_act(x, "both")
     return gemm_fprop(xq, wq), xq, wq
 
 
-def linear_backward(dy: torch.Tensor, xq: QuantAct, wq: QuantWeight,
+def linear_backward(dy: torch.Tensor | QuantAct, xq: QuantAct, wq: QuantWeight,
                     main_grad: torch.Tensor | None = None):
     """Quantize dY both ways, then dX = dY W and dW = dY^T X.  Returns (dx, dw).
+    dY may be a QuantAct already, e.g. from residual_norm_backward or
+    swiglu_backward.
 
     With `main_grad` (FP32 [n, k]) the weight gradient is added into it
     (gradient accumulation across micro-batches) and returned as dw."""
-    dyq = quant_act(dy, "both")
+    dyq = dy if isinstance(dy, QuantAct) else quant_act(dy, "both")
     if main_grad is not None:
         return gemm_dgrad_wgrad(dyq, wq, xq, dw=main_grad, accumulate=True)
     return gemm_dgrad_wgrad(dyq, wq, xq)

@@ -81,7 +81,17 @@ typedef enum {
 enum {
     PURO_ROWWISE = 1,  /* groups of 128 along cols, codes kept in place          */
     PURO_COLWISE = 2,  /* groups of 128 along rows, codes written transposed     */
-    PURO_BOTH = 3      /* both outputs from one read of x                         */
+    PURO_BOTH = 3,     /* both outputs from one read of x                         */
+    PURO_BF16 = 4      /* no codes: the BF16 tensor they would encode (norms, gated
+                          activation only)                                        */
+};
+
+/* Shapes of the gate of puro_fp8_residual_norm. */
+enum {
+    PURO_GATE_NONE = 0,
+    PURO_GATE_TOKEN = 1,    /* one value per token   : BF16 or FP32 [rows]         */
+    PURO_GATE_CHANNEL = 2,  /* one value per channel : BF16 or FP32 [cols]         */
+    PURO_GATE_FULL = 3      /* one per element       : BF16 [rows, cols]           */
 };
 
 /* Bytes of a blocked scale array for `rows` rows and `groups` groups
@@ -282,6 +292,86 @@ PURO_API int puro_fp8_gemm_dgrad_wgrad(const void* qdy, int64_t ld_qdy, const vo
                                        void* dw, int64_t ld_dw,
                                        int64_t m, int64_t n, int64_t k, int dw_kind,
                                        void* stream);
+
+/*
+ * puro_fp8_residual_norm -- the norms around a block, its gate and residual
+ * sum, and the FP8 quantization of the next linear layer's input, in one pass.
+ * (The pages keep the hidden and residual flow and the norms in BF16 around
+ * E4M3 linear layers: paperlayer.ai Appendix C.)
+ *   hh = h * r1[token],  r1 = rsqrt(mean(h^2) + eps)  (w_post NULL: hh = h)
+ *   y  = bf16(x + scale * gate * hh * w_post)         (h NULL: y is x)
+ *   n  = bf16(y * r2[token] * w_pre),  r2 = rsqrt(mean(y^2) + eps), of the stored y
+ * with FP32 sums and factors.  n leaves as codes and scales exactly as
+ * puro_fp8_quant_act makes them of that BF16 tensor (layout PURO_ROWWISE,
+ * PURO_COLWISE or PURO_BOTH; q, s, qt, st as there), or as itself (PURO_BF16: n).
+ * x, h      : BF16 [rows, cols], row strides ld_x, ld_h; h NULL: no block output,
+ *             and w_post, gate, y are ignored.
+ * w_pre, w_post : [cols], both BF16 (w_f32 = 0) or both FP32 (1); w_post may be NULL.
+ * gate      : by gate_kind; ld_gate is the row stride of PURO_GATE_FULL; gate_f32
+ *             selects FP32 for the other two kinds.
+ * y         : BF16 [rows, cols], written; may be x (or h) itself.
+ * rstd, rstd_post : FP32 [rows], r2 and (with w_post) r1, for the backward pass.
+ * cols % 128 == 0, cols <= 8192; any rows >= 0; eps > 0 (PURO_ERR_SHAPE).
+ */
+PURO_API int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t ld_h,
+                                    const void* w_pre, const void* w_post, int w_f32,
+                                    const void* gate, int64_t ld_gate, int gate_kind, int gate_f32,
+                                    float scale, float eps, int64_t rows, int64_t cols,
+                                    void* y, int64_t ld_y, float* rstd, float* rstd_post, int layout,
+                                    void* q, int64_t ld_q, void* s, void* qt, int64_t ld_qt, void* st,
+                                    void* n, int64_t ld_n, void* stream);
+
+/* Bytes of the workspace of puro_fp8_residual_norm_backward (16-byte aligned;
+ * its contents before and after a call mean nothing); 0 for an empty input. */
+PURO_API int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * puro_fp8_residual_norm_backward -- gradients of puro_fp8_residual_norm, from
+ * dn (the gradient of n: the next linear's data gradient) and dy (the gradient
+ * that reaches y from further on; may be NULL).  With t = dn * w_pre,
+ * nh = y * rstd and the forward pass's hh:
+ *   dY = dy + rstd * (t - nh * mean(t nh));  dx = bf16(dY)
+ *   dh = bf16(r1 * (u - hh * mean(u hh))),  u = scale * gate * w_post * dY
+ *        (w_post NULL: dh = bf16(u)) -- the dY of the linear before: as codes, or
+ *        as BF16 with PURO_BF16.  None without h (layout is then only checked).
+ *   dw_pre  = sum_tokens dn * nh,  dw_post = sum_tokens scale * gate * dY * hh
+ *   dgate   = scale * dY * hh * w_post, summed to the gate's shape: FP32 [rows]
+ *        (token), FP32 [cols] (channel), BF16 [rows, cols] with row stride
+ *        ld_dgate (full).
+ * y, rstd, h, rstd_post, weights, gate, scale: as the forward pass had or gave
+ * them.  dx may be dn, dy or y itself.
+ * accumulate == 1 adds dw_pre, dw_post and a channel gate's gradient to what
+ * their FP32 buffers hold (once per element and call, in a fixed order, so
+ * results repeat); 0 overwrites.  rows == 0 writes their zeros.
+ */
+PURO_API int puro_fp8_residual_norm_backward(
+    const void* dn, int64_t ld_dn, const void* dy, int64_t ld_dy, const void* y, int64_t ld_y,
+    const float* rstd, const void* h, int64_t ld_h, const float* rstd_post, const void* w_pre,
+    const void* w_post, int w_f32, const void* gate, int64_t ld_gate, int gate_kind, int gate_f32,
+    float scale, int64_t rows, int64_t cols, void* dx, int64_t ld_dx, float* dw_pre, float* dw_post,
+    void* dgate, int64_t ld_dgate, int accumulate, int layout, void* q, int64_t ld_q, void* s,
+    void* qt, int64_t ld_qt, void* st, void* dh, int64_t ld_dh, void* workspace, void* stream);
+
+/*
+ * puro_fp8_swiglu -- a = bf16(g * sigmoid(g) * u) of the fused gate+up
+ * projection's output gu = [g | u] (BF16 [rows, 2f], row stride ld_gu), as the
+ * FP8 input of the down projection: codes and scales of a [rows, f] as
+ * puro_fp8_quant_act makes them, or a itself (PURO_BF16).  f % 128 == 0.
+ */
+PURO_API int puro_fp8_swiglu(const void* gu, int64_t ld_gu, int64_t rows, int64_t f, int layout,
+                             void* q, int64_t ld_q, void* s, void* qt, int64_t ld_qt, void* st,
+                             void* a, int64_t ld_a, void* stream);
+
+/*
+ * puro_fp8_swiglu_backward -- dgu = [dg | du] from da (BF16 [rows, f], the down
+ * projection's data gradient) and gu: with s = sigmoid(g),
+ *   dg = bf16(da * u * s * (1 + g * (1 - s))),  du = bf16(da * g * s)
+ * as the FP8 dY of the gate+up projection (codes of [rows, 2f]), or as BF16.
+ */
+PURO_API int puro_fp8_swiglu_backward(const void* da, int64_t ld_da, const void* gu, int64_t ld_gu,
+                                      int64_t rows, int64_t f, int layout, void* q, int64_t ld_q,
+                                      void* s, void* qt, int64_t ld_qt, void* st, void* dgu,
+                                      int64_t ld_dgu, void* stream);
 
 /*
  * Support calls (error reporting and self-tests of this library; the pages
