@@ -48,6 +48,8 @@ EXPORTS = (
     "puro_fp8_residual_norm_backward",
     "puro_fp8_swiglu",
     "puro_fp8_swiglu_backward",
+    "puro_fp8_orthogonalize_workspace_bytes",
+    "puro_fp8_orthogonalize",
     "puro_fp8_device_status",
     "puro_fp8_status_string",
     "puro_fp8_test_bounded_wait",
@@ -94,6 +96,9 @@ def load() -> ctypes.CDLL:
                                                     P, I, P, P, P, I, INT, *codes, P, P]
     lib.puro_fp8_swiglu.argtypes = [P, I, I, I, *codes, P]
     lib.puro_fp8_swiglu_backward.argtypes = [P, I, P, I, I, I, *codes, P]
+    lib.puro_fp8_orthogonalize_workspace_bytes.argtypes = [I, I]
+    lib.puro_fp8_orthogonalize_workspace_bytes.restype = I
+    lib.puro_fp8_orthogonalize.argtypes = [P, I, INT, I, I, INT, F, F, F, F, P, I, P, P]
     lib.puro_fp8_device_status.argtypes = [P]
     lib.puro_fp8_status_string.argtypes = [INT]
     lib.puro_fp8_status_string.restype = ctypes.c_char_p
@@ -170,6 +175,14 @@ def puro_fp8_swiglu(*args) -> int:
 
 def puro_fp8_swiglu_backward(*args) -> int:
     return load().puro_fp8_swiglu_backward(*args)
+
+
+def puro_fp8_orthogonalize_workspace_bytes(n, k) -> int:
+    return load().puro_fp8_orthogonalize_workspace_bytes(n, k)
+
+
+def puro_fp8_orthogonalize(g, ld_g, g_f32, n, k, steps, a, b, c, eps, out, ld_out, workspace, stream) -> int:
+    return load().puro_fp8_orthogonalize(g, ld_g, g_f32, n, k, steps, a, b, c, eps, out, ld_out, workspace, stream)
 
 
 def puro_fp8_device_status(stream) -> int:

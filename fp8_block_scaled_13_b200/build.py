@@ -10,7 +10,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libpuro_fp8.so")
 SOURCES = ["puro_fp8.cu"]
-DEPS = ["puro_fp8.cu", "common.cuh", "quant.cuh", "gemm.cuh", "norm.cuh", "gated.cuh"]
+DEPS = ["puro_fp8.cu", "common.cuh", "quant.cuh", "gemm.cuh", "norm.cuh", "gated.cuh",
+        "ortho.cuh"]
 HEADER = os.path.join(ROOT, "include", "puro_fp8.h")
 
 

@@ -373,6 +373,30 @@ PURO_API int puro_fp8_swiglu_backward(const void* da, int64_t ld_da, const void*
                                       void* s, void* qt, int64_t ld_qt, void* st, void* dgu,
                                       int64_t ld_dgu, void* stream);
 
+/* Bytes of the workspace of puro_fp8_orthogonalize for an [n, k] gradient
+ * (256-byte aligned; its contents before and after a call mean nothing; calls
+ * that may run at the same time need distinct ones); 0 for sizes the call does
+ * not take. */
+PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
+
+/*
+ * puro_fp8_orthogonalize -- the Newton-Schulz orthogonalisation of a weight
+ * update, as the Muon optimiser of the pages' recipe takes it
+ * (paper.rainbus.top summary, background on Muon):
+ *   X0 = G / (|G|_F + eps);  steps times X <- a X + (b M + c M^2) X, M = X X^T
+ * (for n > k on the other side: M = X^T X, X <- a X + X (b M + c M^2)).
+ * g    : [n, k] FP32 (g_f32 = 1, e.g. a main gradient) or BF16 (0), any row
+ *        stride ld_g >= k and any alignment of its type; |g| below 1e18 (its
+ *        squares are summed in FP32).
+ * out  : BF16 [n, k], any row stride ld_out >= k; must not overlap g.
+ * Every matrix between is held to 16 significant bits (two BF16 terms), every
+ * product accumulates in FP32, and out is rounded to BF16 once.
+ * 1 <= n, k <= 65536 (0: no-op); 1 <= steps <= 64; eps >= 0.
+ */
+PURO_API int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, int64_t n, int64_t k,
+                                    int steps, float a, float b, float c, float eps, void* out,
+                                    int64_t ld_out, void* workspace, void* stream);
+
 /*
  * Support calls (error reporting and self-tests of this library; the pages
  * have no counterpart).
