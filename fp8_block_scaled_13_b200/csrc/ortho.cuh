@@ -1,33 +1,43 @@
 // Orthogonalising a weight update by Newton-Schulz products, as the Muon
 // optimiser does (Jordan et al., "Muon", 2024: a quintic iteration):
-//   X0 = G / (|G|_F + eps);   steps times:  M = X X^T,  P = a I + b M + c M^2,  X <- P X
+//   X0 = G / (|G|_F + eps);   steps times:  M = X X^T,  R = b M + c M^2,  X <- a X + R X
 // on the smaller side of G: for a tall G (more rows than columns) M = X^T X
-// and X <- X P.
+// and X <- a X + X R.
 //
-// Precision.  The iteration multiplies small singular values by up to a = 3.4
-// a step while it cancels large terms (3.4 - 4.8 + 2.0) in the large ones, so
-// operand roundings come out amplified: with BF16 operands the result is off
-// by 1e-2 (Gaussian G) to 0.17 (a few strong directions over a floor, as
-// gradients have), with FP16 ones by 2e-3 to 2e-2, against 1.7e-3 for the
-// rounding of the BF16 result.  So every operand is held as two BF16 terms,
-// hi + lo (16 significant bits), and each product takes three tensor-core
-// products, hi hi + hi lo + lo hi, into one FP32 accumulator: off by 1.5e-5
-// to 2.5e-4.  A BF16 G is exact in one term and takes fewer products.
+// Precision.  The iteration lifts small singular values by up to a = 3.4 a
+// step while it cancels large terms (3.4 - 4.8 + 2.0) in the large ones, so a
+// rounding of X that the next step sees as part of X comes out amplified:
+// with all operands in BF16 the result is off by 1e-2 (Gaussian G) to 0.17 (a
+// few strong directions over a floor, as gradients have), against 1.7e-3 for
+// the rounding of the BF16 result.  Here X is held as two FP16 terms, hi + lo
+// (22 significant bits), and only what enters a product is rounded to FP16,
+// off the diagonal: with M = D + O and R = D' + O' (D, D' diagonal, in FP32)
+//   M^2 = O O + D O + O D + D^2,      a X + R X = (a + D') X + O' X,
+// the tensor cores compute X X^T, O O and O' X from FP16 operands, one product
+// each, and the epilogues add the rest in FP32 from the exact parts.  What the
+// operands lose is random and averaged over the long sums, and the large,
+// coherent parts -- the diagonals, and X itself -- are not rounded at all: off by
+// 3e-4 to 8e-4 for Gaussian, low-rank, power-law and geometric spectra.  (Two
+// BF16 terms per operand and three products each were as exact and took twice
+// as long: 2168 us against 1133 for 12288 x 2048.)  A short sum averages
+// less, so X X^T over up to kOrthoExactK takes three products, hi hi + hi lo +
+// lo hi, where launches and not products are the time anyway.
+// Powers of two keep FP16 in range: X is stored times 2^10, M times 2^13, R
+// times 2^12, which holds while |X| < 64, |M| < 8 and |R| < 16 off the
+// diagonal; the iteration keeps singular values near 1.
 //
 // All three products of a step are one kernel, D[i, j] = sum_k P[i, k] Q[j, k]:
-// tcgen05 kind::f16 on CTA pairs (256-row tiles), fed by TMA through a ring of
-// 64-deep stages that hold the hi and lo tiles of both operands -- four tiles
-// loaded for three products.  An operand that is stored the other way round
-// ([k][i]) is read MN-major, so nothing is ever transposed in memory.  M and
-// P are symmetric: only tiles on or below the diagonal are computed and the
-// epilogue writes each one also to its mirrored place; with 256 x 128 tiles a
-// 2048-wide M is 72 units, one wave of the 74 CTA pairs.  The norm of G
-// scales the first M (by its square) and the first X in the epilogue, so G is
-// read once to split it.  Bound by the tensor cores for large G, by launches
-// (1 + 3 steps, overlapped by programmatic dependent launch) for small ones.
+// tcgen05 kind::f16 on CTA pairs (256-row tiles), FP32 accumulators in TMEM,
+// fed by TMA.  An operand that is stored the other way round ([k][i]) is read
+// MN-major, so nothing is ever transposed in memory.  M and R are symmetric:
+// only tiles on or below the diagonal are computed and the epilogue writes
+// each one also to its mirrored place; with 256 x 128 tiles a 2048-wide M is 72
+// units, one wave of the 74 CTA pairs.  Bound by the tensor cores for large G, by launches
+// (2 + 3 steps, overlapped by programmatic dependent launch) for small ones.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
@@ -35,33 +45,36 @@ namespace puro {
 
 enum OrthoEpilogue : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2 };
 
-constexpr int kOrthoNormBlocks = 592;  // CTAs of the splitting pass, one partial sum each
+constexpr int kOrthoNormBlocks = 592;  // CTAs of the norm pass, one partial sum each
+constexpr int64_t kOrthoExactK = 1024; // longest X X^T sum that takes three products
+constexpr float kXScale = 1024.f, kMScale = 8192.f, kRScale = 4096.f;
 
 struct OrthoParams {
   int32_t rows_a, rows_b;   // D is [rows_a, rows_b]
   int32_t kblocks;          // ceil(K / 64)
+  int32_t passes;           // 1: hi hi; 3: hi hi, hi lo, lo hi
   int32_t tiles_m, tiles_n;
   int32_t units;            // tiles; kOrthoGram / kOrthoPoly: those on or below the diagonal
-  int32_t terms_a, terms_b; // 2: hi and lo, 1: hi only (lo is zero)
-  float alpha, beta, diag;  // kOrthoPoly: alpha acc + beta M + diag I
-  const __nv_bfloat16* m_hi;
-  const __nv_bfloat16* m_lo;
-  int64_t ld_m;
-  const float* norm_part;   // kOrthoNormBlocks sums of squares of G, or null (already normalised)
-  float eps;
-  __nv_bfloat16* out;       // last step: the BF16 result, by plain stores if out_tma is 0
+  float a, b, c;
+  float* diag;              // Gram: D written; Poly: D read
+  float* diag_r;            // Poly: D' written; Update: D' read
+  const __half* src_hi;     // Poly: O (times 2^13); Update: X hi
+  const __half* src_lo;     // Update: X lo
+  int64_t ld_src;
+  __nv_bfloat16* out;       // last step: the BF16 result
   int64_t ld_out;
-  int32_t last, out_tma;
+  int32_t col_diag;         // Update: D' goes by column (tall G)
+  int32_t last, out_tma;    // last step; the result goes out by TMA (else by plain stores)
 };
 
 template <int BN>
 struct OrthoCfg {
   static constexpr int kBM = 256;              // tile rows (a CTA pair)
   static constexpr int kBNC = BN / 2;          // rows of Q in each CTA
-  static constexpr uint32_t kTileA = 128 * 128;       // 128 rows x 64 BF16
+  static constexpr uint32_t kTileA = 128 * 128;       // 128 rows x 64 FP16
   static constexpr uint32_t kTileB = kBNC * 128;
-  static constexpr uint32_t kStageBytes = 2 * (kTileA + kTileB);
-  static constexpr int kStages = BN == 256 ? 3 : 4;   // 192 KB
+  static constexpr uint32_t kStageBytes = kTileA + kTileB;
+  static constexpr int kStages = BN == 256 ? 6 : 8;   // 192 KB
   static constexpr int kEpiWarps = 8;
   static constexpr int kEpiCols = BN / 2;
   static constexpr uint32_t kEpiBytes = kEpiWarps * 4096;  // hi and lo, 32 rows x 64 bytes each
@@ -75,8 +88,8 @@ struct OrthoCfg {
   static constexpr uint32_t kTmemCols = 2 * BN;       // two accumulators
 };
 
-// D[tmem] (+)= A B^T for one M = 256, K = 16 slice of BF16 operands of the CTA pair.
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// D[tmem] (+)= A B^T for one M = 256, K = 16 slice of FP16 operands of the CTA pair.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -114,19 +127,13 @@ __device__ __forceinline__ void ortho_tile(const OrthoParams& p, int u, int& tm,
   }
 }
 
-// 1 / (|G|_F + eps) from the partial sums, by a converged warp.
-__device__ __forceinline__ float ortho_scale(const OrthoParams& p, int lane) {
-  if (!p.norm_part) return 1.f;
-  float s = 0.f;
-  for (int i = lane; i < kOrthoNormBlocks; i += 32) s += p.norm_part[i];
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-  return 1.f / (sqrtf(s) + p.eps);
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
+__device__ __forceinline__ float2 half_unpack(uint32_t w) {
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
 template <int BN, bool AMN, bool BMN, int EPI>
@@ -138,8 +145,8 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
   using C = OrthoCfg<BN>;
   constexpr int S = C::kStages;
   constexpr bool SYM = EPI != kOrthoUpdate;
-  // D FP32, A and B BF16, MN-major flags, N, M
-  constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
+  // D FP32, A and B FP16 (formats 0), MN-major flags, N, M
+  constexpr uint32_t kIdesc = (1u << 4) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
                               ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(C::kBM >> 4) << 24);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -190,38 +197,33 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
     // ------------------------------------------------------------ producer
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
-    const uint32_t tx = 2 * (p.terms_a * C::kTileA + p.terms_b * C::kTileB);
     bool ok = true;
     for (int u = cluster_id; u < p.units && ok; u += clusters) {
       int tm, tn;
       ortho_tile<SYM>(p, u, tm, tn);
       const int a0 = tm * C::kBM + 128 * (int)rank;
       const int b0 = tn * BN + C::kBNC * (int)rank;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int i = 0; i < p.kblocks * p.passes; ++i) {
+        const int pass = i / p.kblocks, k0 = (i - pass * p.kblocks) * 64;
         if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(&full[stage], tx);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
           const uint32_t bar = leader_addr<2>(&full[stage]);
-          uint8_t* st = smem + stage * C::kStageBytes;
-          const int k0 = kb * 64;
-          for (int t = 0; t < p.terms_a; ++t) {
-            const CUtensorMap* m = t ? &tm_al : &tm_ah;
-            uint8_t* d = st + t * C::kTileA;
-            if (AMN) {
-              tma_load_2d<2>(d, m, a0, k0, bar);
-              tma_load_2d<2>(d + 8192, m, a0 + 64, k0, bar);
-            } else {
-              tma_load_2d<2>(d, m, k0, a0, bar);
-            }
+          uint8_t* da = smem + stage * C::kStageBytes;
+          uint8_t* db = da + C::kTileA;
+          const CUtensorMap* ma = pass == 2 ? &tm_al : &tm_ah;
+          const CUtensorMap* mb = pass == 1 ? &tm_bl : &tm_bh;
+          if (AMN) {
+            tma_load_2d<2>(da, ma, a0, k0, bar);
+            tma_load_2d<2>(da + 8192, ma, a0 + 64, k0, bar);
+          } else {
+            tma_load_2d<2>(da, ma, k0, a0, bar);
           }
-          for (int t = 0; t < p.terms_b; ++t) {
-            const CUtensorMap* m = t ? &tm_bl : &tm_bh;
-            uint8_t* d = st + 2 * C::kTileA + t * C::kTileB;
-            if (BMN) {
-              for (int h = 0; h < C::kBNC / 64; ++h) tma_load_2d<2>(d + 8192 * h, m, b0 + 64 * h, k0, bar);
-            } else {
-              tma_load_2d<2>(d, m, k0, b0, bar);
-            }
+          if (BMN) {
+#pragma unroll
+            for (int h = 0; h < C::kBNC / 64; ++h) tma_load_2d<2>(db + 8192 * h, mb, b0 + 64 * h, k0, bar);
+          } else {
+            tma_load_2d<2>(db, mb, k0, b0, bar);
           }
         }
         issued_mask |= 1u << stage;
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
       bool ok = true;
       const uint32_t base = smem_u32(smem);
       const uint64_t a_desc0 = AMN ? desc_sw128_mnmajor(base) : desc_sw128_kmajor(base);
-      const uint64_t b_desc0 = BMN ? desc_sw128_mnmajor(base + 2 * C::kTileA) : desc_sw128_kmajor(base + 2 * C::kTileA);
+      const uint64_t b_desc0 = BMN ? desc_sw128_mnmajor(base + C::kTileA) : desc_sw128_kmajor(base + C::kTileA);
       constexpr uint32_t kStepA = AMN ? 2048 >> 4 : 32 >> 4;  // 16 elements along k
       constexpr uint32_t kStepB = BMN ? 2048 >> 4 : 32 >> 4;
       for (int u = cluster_id; u < p.units && ok; u += clusters, ++it) {
@@ -253,24 +255,15 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
         if (!mbar_wait_warp(&acce[acc], ((it >> 1) & 1) ^ 1, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int i = 0; i < p.kblocks * p.passes; ++i) {
           if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ah = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
-            const uint64_t bh = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
-            const uint64_t al = ah + (C::kTileA >> 4), bl = bh + (C::kTileB >> 4);
+            const uint64_t ad = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+            const uint64_t bd = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_bf16(d, ah + k * kStepA, bh + k * kStepB, kIdesc, (kb | k) != 0 ? 1u : 0u);
-            if (p.terms_b > 1) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) tc_mma_bf16(d, ah + k * kStepA, bl + k * kStepB, kIdesc, 1u);
-            }
-            if (p.terms_a > 1) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) tc_mma_bf16(d, al + k * kStepA, bh + k * kStepB, kIdesc, 1u);
-            }
+              tc_mma_f16(d, ad + k * kStepA, bd + k * kStepB, kIdesc, (i | k) != 0 ? 1u : 0u);
             tc_commit_all<2>(&empty[stage]);
           }
           if (++stage == S) { stage = 0; phase ^= 1; }
@@ -288,11 +281,9 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
     const int sp = warp & 3, half = (warp - 2) >> 2;
     uint8_t* buf_h = smem + C::kOffEpi + (warp - 2) * 4096;
     uint8_t* buf_l = buf_h + 2048;
-    float scale = 1.f;
-    if (EPI != kOrthoPoly) scale = ortho_scale(p, lane);
-    if (EPI == kOrthoGram) scale *= scale;
-    // hands a staged 32 x 32 pair of tiles to TMA; `again` waits until the
-    // buffers may be written once more
+    constexpr int kChunks = C::kEpiCols / 32;
+    constexpr int kSrc = EPI == kOrthoUpdate ? 8 : 4;  // 16-byte words of the source per thread and chunk
+    // hands a staged pair of 32 x 32 tiles to TMA
     auto store = [&](int x, int y, bool low) {
       fence_proxy_async_smem();
       __syncwarp();
@@ -302,9 +293,21 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
         bulk_commit_group();
       }
     };
+    // waits until the buffers may be written once more
     auto again = [&]() {
       if (lane == 0) bulk_wait_group_read<0>();
       __syncwarp();
+    };
+    // this thread's row of a chunk of the source: O, or X hi and X lo
+    auto load_src = [&](int row, int col0, uint4 (&v)[8]) {
+      if (EPI == kOrthoGram) return;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool in = row < p.rows_a && col0 + 8 * q < p.rows_b;
+        const int64_t at = (int64_t)row * p.ld_src + col0 + 8 * q;
+        v[q] = in ? *reinterpret_cast<const uint4*>(p.src_hi + at) : make_uint4(0, 0, 0, 0);
+        if (kSrc == 8) v[4 + q] = in ? *reinterpret_cast<const uint4*>(p.src_lo + at) : make_uint4(0, 0, 0, 0);
+      }
     };
     int it = 0;
     for (int u = cluster_id; u < p.units; u += clusters, ++it) {
@@ -313,17 +316,26 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
       const int acc = it & 1;
       const int row0 = tm * C::kBM + 128 * (int)rank + sp * 32;
       const int row = row0 + lane;
+      const int colh = tn * BN + half * C::kEpiCols;
       const bool mirror = SYM && (tn >> 1) < tm;
+      uint4 src[8];
+      load_src(row, colh, src);
+      const float dr = row < p.rows_a ? (EPI == kOrthoPoly ? p.diag[row] : EPI == kOrthoUpdate && !p.col_diag ? p.diag_r[row] : 0.f) : 0.f;
       if (!mbar_wait_warp(&accf[acc], (it >> 1) & 1, abort_flag)) break;
       tc_fence_after();
       const uint32_t t_base = tmem + ((uint32_t)(sp * 32) << 16) + acc * BN + half * C::kEpiCols;
-      for (int c = 0; c < C::kEpiCols / 32; ++c) {
-        const int col0 = tn * BN + half * C::kEpiCols + c * 32;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int col0 = colh + c * 32;
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_base + c * 32, r);
+        uint4 cur[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) cur[q] = src[q];
+        if (c + 1 < kChunks) load_src(row, col0 + 32, src);
         tmem_ld_wait();
         regs_after_wait(r);
-        if (c == C::kEpiCols / 32 - 1) {
+        if (c == kChunks - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_leader<2>(&acce[acc]);
@@ -331,68 +343,109 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
         if (row0 >= p.rows_a || col0 >= p.rows_b) continue;
         float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * (EPI == kOrthoPoly ? p.alpha : scale);
-        if (EPI == kOrthoPoly) {
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+        if (EPI == kOrthoGram) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[e] *= kMScale / (kXScale * kXScale);
+            if (row == col0 + e) {
+              if (row < p.rows_a) p.diag[row] = v[e] * (1.f / kMScale);
+              v[e] = 0.f;
+            }
+          }
+        }
+        if (EPI != kOrthoGram) {
+          // D or D' of the columns
+          const float* dp = EPI == kOrthoPoly ? p.diag : p.diag_r;
+          const float dc = (EPI == kOrthoPoly || p.col_diag) && col0 + lane < p.rows_b ? dp[col0 + lane] : 0.f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (row < p.rows_a && col0 + 8 * q < p.rows_b) {
-              const uint4 h = *reinterpret_cast<const uint4*>(p.m_hi + (int64_t)row * p.ld_m + col0 + 8 * q);
-              const uint4 l = *reinterpret_cast<const uint4*>(p.m_lo + (int64_t)row * p.ld_m + col0 + 8 * q);
-              const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+            const uint32_t hw[4] = {cur[q].x, cur[q].y, cur[q].z, cur[q].w};
+            const uint32_t lw[4] = {cur[4 + q].x, cur[4 + q].y, cur[4 + q].z, cur[4 + q].w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float m0 = __uint_as_float(hw[e] << 16) + __uint_as_float(lw[e] << 16);
-                const float m1 = __uint_as_float(hw[e] & 0xFFFF0000u) + __uint_as_float(lw[e] & 0xFFFF0000u);
-                v[8 * q + 2 * e] = fmaf(p.beta, m0, v[8 * q + 2 * e]);
-                v[8 * q + 2 * e + 1] = fmaf(p.beta, m1, v[8 * q + 2 * e + 1]);
+            for (int w = 0; w < 4; ++w) {
+              const int e = 8 * q + 2 * w;
+              const float2 h = half_unpack(hw[w]);
+              const float d0 = __shfl_sync(0xFFFFFFFFu, dc, e), d1 = __shfl_sync(0xFFFFFFFFu, dc, e + 1);
+              if (EPI == kOrthoPoly) {
+                // R = c (O O + O (D_i + D_j)) + b O off the diagonal
+                v[e] = fmaf(v[e], p.c * (kRScale / (kMScale * kMScale)), h.x * (kRScale / kMScale) * fmaf(p.c, dr + d0, p.b));
+                v[e + 1] = fmaf(v[e + 1], p.c * (kRScale / (kMScale * kMScale)), h.y * (kRScale / kMScale) * fmaf(p.c, dr + d1, p.b));
+              } else {
+                const float2 l = half_unpack(lw[w]);
+                v[e] = fmaf(p.a + dr + d0, h.x + l.x, v[e] * (1.f / kRScale));
+                v[e + 1] = fmaf(p.a + dr + d1, h.y + l.y, v[e + 1] * (1.f / kRScale));
               }
             }
           }
+          if (EPI == kOrthoPoly) {
+            // on it, D' = c ((O O)_ii + D_i^2) + b D_i
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (row == col0 + e) v[e] += p.diag;
+            for (int e = 0; e < 32; ++e)
+              if (row == col0 + e) {
+                if (row < p.rows_a)
+                  p.diag_r[row] = fmaf(__uint_as_float(r[e]), p.c / (kMScale * kMScale), dr * fmaf(p.c, dr, p.b));
+                v[e] = 0.f;
+              }
+          }
         }
-        // hi and lo of each pair of columns
-        uint32_t hi[16], lo[16];
+        if (EPI == kOrthoUpdate && p.last) {
+          uint32_t o[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          hi[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
-          lo[e] = bf16_pair(v[2 * e] - __uint_as_float(hi[e] << 16),
-                            v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-        }
-        if (EPI == kOrthoUpdate && p.last && !p.out_tma) {
-          // a result whose rows do not start on 16-byte boundaries: plain
-          // stores, a row at a time through shared memory
-          __syncwarp();
+          for (int e = 0; e < 16; ++e) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e] * (1.f / kXScale), v[2 * e + 1] * (1.f / kXScale));
+            o[e] = *reinterpret_cast<uint32_t*>(&h);
+          }
+          again();
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(buf_h + lane * 64 + 16 * q) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-          __syncwarp();
-          for (int y = 0; y < 32 && row0 + y < p.rows_a; ++y)
-            if (col0 + lane < p.rows_b)
-              p.out[(int64_t)(row0 + y) * p.ld_out + col0 + lane] = reinterpret_cast<const __nv_bfloat16*>(buf_h)[y * 32 + lane];
+            *reinterpret_cast<uint4*>(buf_h + lane * 64 + 16 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          if (p.out_tma) {
+            store(col0, row0, false);
+          } else {
+            // rows that do not start on 16-byte boundaries: plain stores
+            __syncwarp();
+            for (int y = 0; y < 32 && row0 + y < p.rows_a; ++y)
+              if (col0 + lane < p.rows_b)
+                p.out[(int64_t)(row0 + y) * p.ld_out + col0 + lane] = reinterpret_cast<const __nv_bfloat16*>(buf_h)[y * 32 + lane];
+            __syncwarp();
+          }
           continue;
         }
-        const bool low = !(EPI == kOrthoUpdate && p.last);
+        uint32_t hi[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hi[e] = half_pair(v[2 * e], v[2 * e + 1]);
         again();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           *reinterpret_cast<uint4*>(buf_h + lane * 64 + 16 * q) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-          *reinterpret_cast<uint4*>(buf_l + lane * 64 + 16 * q) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+          if (EPI == kOrthoUpdate) {
+            uint32_t lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 h = half_unpack(hi[4 * q + e]);
+              lo[e] = half_pair(v[8 * q + 2 * e] - h.x, v[8 * q + 2 * e + 1] - h.y);
+            }
+            *reinterpret_cast<uint4*>(buf_l + lane * 64 + 16 * q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
-        store(col0, row0, low);
-        if (mirror) {
-          again();
+        if (SYM && mirror) {
+          // the transposed tile beside it, in the second buffer
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            uint16_t* h = reinterpret_cast<uint16_t*>(buf_h) + 64 * e + lane;
-            uint16_t* l = reinterpret_cast<uint16_t*>(buf_l) + 64 * e + lane;
-            h[0] = static_cast<uint16_t>(hi[e]);
-            h[32] = static_cast<uint16_t>(hi[e] >> 16);
-            l[0] = static_cast<uint16_t>(lo[e]);
-            l[32] = static_cast<uint16_t>(lo[e] >> 16);
+            uint16_t* t = reinterpret_cast<uint16_t*>(buf_l) + 64 * e + lane;
+            t[0] = static_cast<uint16_t>(hi[e]);
+            t[32] = static_cast<uint16_t>(hi[e] >> 16);
           }
-          store(row0, col0, true);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_dh, buf_h, col0, row0);
+            tma_store_2d(&tm_dh, buf_l, row0, col0);
+            bulk_commit_group();
+          }
+        } else {
+          store(col0, row0, EPI == kOrthoUpdate);
         }
       }
     }
@@ -406,33 +459,62 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
   if (warp == 1) tmem_dealloc<2>(tmem, C::kTmemCols);
 }
 
-// Splits G [n, k] into BF16 hi + lo (F32) or copies it (BF16, COPY), and sums
-// its squares: one partial sum per CTA, in a fixed order.
+// The two passes that make X0.  The first sums the squares of G [n, k], one
+// partial sum per CTA in a fixed order; the second writes 2^10 G / (|G|_F + eps)
+// as FP16 hi + lo.  VEC: rows start on 16-byte boundaries.
 struct OrthoSplitParams {
   const void* g;
-  int64_t ld_g, n, k, ld_x;
-  __nv_bfloat16* hi;
-  __nv_bfloat16* lo;
+  int64_t ld_g, ld_x;
+  int32_t n, k;
+  float eps;
+  __half* hi;
+  __half* lo;
   float* part;   // [kOrthoNormBlocks]
 };
 
-template <bool F32, bool COPY>
-__global__ void __launch_bounds__(256) ortho_split_kernel(const OrthoSplitParams p) {
+// Up to 8 values of a row from column c on, zeros past the end.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_g8(const OrthoSplitParams& p, int64_t r, int32_t c, float (&v)[8]) {
+  if (VEC && c + 8 <= p.k) {
+    if (F32) {
+      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.g) + r * p.ld_g + c);
+      const float4 a = s[0], b = s[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.g) + r * p.ld_g + c);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = c + i >= p.k ? 0.f
+           : F32        ? static_cast<const float*>(p.g)[r * p.ld_g + c + i]
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.g)[r * p.ld_g + c + i]);
+}
+
+// n ceil(k / 8) pieces fit 32 bits (n, k <= 65536).
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoSplitParams p) {
   __shared__ float sm[8];
   pdl_wait();
   pdl_trigger();
   float s = 0.f;
-  const int64_t total = p.n * p.k, stride = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += stride) {
-    const int64_t r = i / p.k, c = i - r * p.k;
-    const float v = F32 ? static_cast<const float*>(p.g)[r * p.ld_g + c]
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.g)[r * p.ld_g + c]);
-    s = fmaf(v, v, s);
-    if (F32 || COPY) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      p.hi[r * p.ld_x + c] = h;
-      if (F32) p.lo[r * p.ld_x + c] = __float2bfloat16_rn(v - __bfloat162float(h));
-    }
+  const uint32_t per_row = (uint32_t)(p.k + 7) / 8, total = per_row * (uint32_t)p.n;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const uint32_t r = i / per_row;
+    float v[8];
+    load_g8<F32, VEC>(p, r, (int32_t)(i - r * per_row) * 8, v);
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t = fmaf(v[e], v[e], t);
+    s += t;
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
@@ -441,6 +523,34 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const OrthoSplitParams
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) s += sm[w];
     p.part[blockIdx.x] = s;
+  }
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) ortho_split_kernel(const OrthoSplitParams p) {
+  pdl_wait();
+  pdl_trigger();
+  float s = 0.f;  // every warp adds the partial sums in the same order
+  for (int i = threadIdx.x & 31; i < kOrthoNormBlocks; i += 32) s += p.part[i];
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  const float scale = kXScale / (sqrtf(s) + p.eps);
+  const uint32_t per_row = (uint32_t)(p.k + 7) / 8, total = per_row * (uint32_t)p.n;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const uint32_t r = i / per_row, c = (i - r * per_row) * 8;
+    float v[8];
+    load_g8<F32, VEC>(p, r, (int32_t)c, v);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[2 * e] * scale, y = v[2 * e + 1] * scale;
+      h[e] = half_pair(x, y);
+      const float2 f = half_unpack(h[e]);
+      l[e] = half_pair(x - f.x, y - f.y);
+    }
+    // rows of X are padded to multiples of 8, so the whole piece may be written
+    *reinterpret_cast<uint4*>(p.hi + (int64_t)r * p.ld_x + c) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(p.lo + (int64_t)r * p.ld_x + c) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 

@@ -1131,16 +1131,17 @@ namespace {
 constexpr int kOrthoMaxSteps = 64;
 constexpr int64_t kOrthoMaxDim = 65536;
 
-// A BF16 matrix [rows, cols] held as hi + lo (lo == nullptr: exact in hi).
-struct Split {
-  __nv_bfloat16* hi;
-  __nv_bfloat16* lo;
+// An FP16 matrix [rows, cols], of X also its low terms.
+struct OrthoMat {
+  __half* hi;
+  __half* lo;
   int64_t rows, cols, ld;
 };
 
-// Where the workspace of an n x k problem keeps its matrices, in elements.
+// Where the workspace of an n x k problem keeps its matrices.
 struct OrthoLayout {
-  int64_t x_elems, m_elems, ld_x, ld_m;
+  int64_t ld_x, ld_m;
+  int64_t x_elems, m_elems;  // FP16 elements of one matrix, a multiple of 128 (256 bytes)
   int64_t bytes;
 };
 
@@ -1149,48 +1150,51 @@ OrthoLayout ortho_layout(int64_t n, int64_t k) {
   const int64_t m = n < k ? n : k;
   l.ld_x = (k + 7) / 8 * 8;
   l.ld_m = (m + 7) / 8 * 8;
-  l.x_elems = (n * l.ld_x + 127) / 128 * 128;   // every matrix starts on a 256-byte boundary
+  l.x_elems = (n * l.ld_x + 127) / 128 * 128;
   l.m_elems = (m * l.ld_m + 127) / 128 * 128;
-  // two X (read and written in turn), M and P, each as hi and lo; the norm's partial sums
-  l.bytes = (4 * l.x_elems + 4 * l.m_elems) * 2 + puro::kOrthoNormBlocks * (int64_t)sizeof(float);
+  // two X (read and written in turn) as hi and lo; O and O'; D and D'; the norm's partial sums
+  l.bytes = (4 * l.x_elems + 2 * l.m_elems) * 2 + (2 * l.ld_m + puro::kOrthoNormBlocks) * (int64_t)sizeof(float);
   return l;
 }
 
-// [outer, inner] BF16 matrix, boxes of box_inner x box_outer elements.
-int make_map_bf16(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, uint32_t box_inner,
-                  uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+// [outer, inner] 16-bit matrix, boxes of box_inner x box_outer elements.
+int make_map_16(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, uint32_t box_inner,
+                uint32_t box_outer, CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PURO_OK : PURO_ERR_CUDA;
 }
 
-// One product D[i, j] = sum_k P[i, k] Q[j, k] of the iteration; p_mn / q_mn:
-// the operand is stored [k][i] / [k][j].
+// One product D[i, j] = sum_k A[i, k] B[j, k] of the iteration; AMN / BMN: the
+// operand is stored [k][i] / [k][j].
 template <int BN, bool AMN, bool BMN, int EPI>
-int launch_ortho_gemm(const Split& a, const Split& b, const Split& d, puro::OrthoParams p, const DeviceInfo& dev,
+int launch_ortho_gemm(const OrthoMat& a, const OrthoMat& b, const OrthoMat& d, puro::OrthoParams p, const DeviceInfo& dev,
                       cudaStream_t stream) {
   using C = puro::OrthoCfg<BN>;
   CUtensorMap m[6];
   int st;
-  auto operand = [&](CUtensorMap* hi, CUtensorMap* lo, const Split& s, bool mn, uint32_t rows) {
-    const uint32_t box_outer = mn ? 64 : rows;
-    int r = make_map_bf16(hi, s.hi, s.cols, s.rows, s.ld, 64, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (r != PURO_OK) return r;
-    return make_map_bf16(lo, s.lo ? s.lo : s.hi, s.cols, s.rows, s.ld, 64, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
-  };
-  if ((st = operand(&m[0], &m[1], a, AMN, 128)) != PURO_OK) return st;
-  if ((st = operand(&m[2], &m[3], b, BMN, C::kBNC)) != PURO_OK) return st;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
+  if ((st = make_map_16(&m[0], a.hi, a.cols, a.rows, a.ld, 64, AMN ? 64 : 128, sw)) != PURO_OK) return st;
+  if ((st = make_map_16(&m[2], b.hi, b.cols, b.rows, b.ld, 64, BMN ? 64 : C::kBNC, sw)) != PURO_OK) return st;
+  m[1] = m[0];
+  m[3] = m[2];
+  if (p.passes > 1) {
+    if ((st = make_map_16(&m[1], a.lo, a.cols, a.rows, a.ld, 64, AMN ? 64 : 128, sw)) != PURO_OK) return st;
+    if ((st = make_map_16(&m[3], b.lo, b.cols, b.rows, b.ld, 64, BMN ? 64 : C::kBNC, sw)) != PURO_OK) return st;
+  }
+  m[4] = m[5] = m[0];  // not used when the result leaves by plain stores
   if (!p.last || p.out_tma) {
-    if ((st = make_map_bf16(&m[4], d.hi, d.cols, d.rows, d.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != PURO_OK) return st;
-    if ((st = make_map_bf16(&m[5], d.lo ? d.lo : d.hi, d.cols, d.rows, d.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != PURO_OK)
+    const void* hi = p.last ? static_cast<const void*>(p.out) : d.hi;
+    if ((st = make_map_16(&m[4], hi, d.cols, d.rows, d.ld, 32, 32, none)) != PURO_OK) return st;
+    m[5] = m[4];
+    if (EPI == puro::kOrthoUpdate && !p.last &&
+        (st = make_map_16(&m[5], d.lo, d.cols, d.rows, d.ld, 32, 32, none)) != PURO_OK)
       return st;
-  } else {
-    m[4] = m[5] = m[0];  // not used
   }
   p.rows_a = (int32_t)d.rows;
   p.rows_b = (int32_t)d.cols;
@@ -1203,8 +1207,6 @@ int launch_ortho_gemm(const Split& a, const Split& b, const Split& d, puro::Orth
     p.units = 0;
     for (int i = 0; i < p.tiles_m; ++i) p.units += 2 * i + 2 < p.tiles_n ? 2 * i + 2 : p.tiles_n;
   }
-  p.terms_a = a.lo ? 2 : 1;
-  p.terms_b = b.lo ? 2 : 1;
   auto kern = puro::ortho_gemm_kernel<BN, AMN, BMN, EPI>;
   static std::atomic<int> max_clusters[kMaxDevices] = {};
   cudaLaunchConfig_t cfg = {};
@@ -1238,7 +1240,7 @@ int launch_ortho_gemm(const Split& a, const Split& b, const Split& d, puro::Orth
   return PURO_OK;
 }
 
-template <bool F32, bool COPY>
+template <bool F32, bool VEC>
 int launch_ortho_split(const puro::OrthoSplitParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1249,7 +1251,8 @@ int launch_ortho_split(const puro::OrthoSplitParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, puro::ortho_split_kernel<F32, COPY>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, puro::ortho_norm_kernel<F32, VEC>, p) != cudaSuccess ||
+      cudaLaunchKernelEx(&cfg, puro::ortho_split_kernel<F32, VEC>, p) != cudaSuccess) {
     cudaGetLastError();
     return PURO_ERR_CUDA;
   }
@@ -1271,8 +1274,7 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
     return PURO_ERR_SHAPE;
   if (n == 0 || k == 0) return PURO_OK;
   if (!g || !out || !workspace) return PURO_ERR_NULL;
-  if (!aligned_to(g, g_f32 ? 4 : 2) || !aligned_to(out, 2) || reinterpret_cast<uintptr_t>(workspace) % 256)
-    return PURO_ERR_ALIGN;
+  if (!aligned_to(g, g_f32 ? 4 : 2) || !aligned_to(out, 2) || !aligned_to(workspace, 256)) return PURO_ERR_ALIGN;
   if (ld_g < k || ld_out < k) return PURO_ERR_SHAPE;
   DeviceInfo* dev = nullptr;
   int st = current_device(&dev);
@@ -1283,55 +1285,55 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
   const OrthoLayout l = ortho_layout(n, k);
   const bool tall = n > k;
   const int64_t m = tall ? k : n;
-  __nv_bfloat16* base = static_cast<__nv_bfloat16*>(workspace);
-  Split x[2];
-  for (int i = 0; i < 2; ++i) x[i] = Split{base + 2 * i * l.x_elems, base + (2 * i + 1) * l.x_elems, n, k, l.ld_x};
-  __nv_bfloat16* mb = base + 4 * l.x_elems;
-  Split mm{mb, mb + l.m_elems, m, m, l.ld_m}, pp{mb + 2 * l.m_elems, mb + 3 * l.m_elems, m, m, l.ld_m};
-  float* part = reinterpret_cast<float*>(mb + 4 * l.m_elems);
+  __half* base = static_cast<__half*>(workspace);
+  OrthoMat x[2];
+  for (int i = 0; i < 2; ++i) x[i] = OrthoMat{base + 2 * i * l.x_elems, base + (2 * i + 1) * l.x_elems, n, k, l.ld_x};
+  __half* mb = base + 4 * l.x_elems;
+  const OrthoMat mo{mb, nullptr, m, m, l.ld_m}, ro{mb + l.m_elems, nullptr, m, m, l.ld_m};
+  float* diag = reinterpret_cast<float*>(mb + 2 * l.m_elems);
+  float* diag_r = diag + l.ld_m;
 
-  // X0: the split gradient, or a BF16 gradient where it lies
-  Split cur = x[0];
-  puro::OrthoSplitParams sp{g, ld_g, n, k, l.ld_x, cur.hi, cur.lo, part};
-  if (g_f32) {
-    st = launch_ortho_split<true, true>(sp, sm);
-  } else if (aligned16(g) && ld_g % 8 == 0) {
-    cur = Split{const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(g)), nullptr, n, k, ld_g};
-    st = launch_ortho_split<false, false>(sp, sm);
-  } else {
-    cur.lo = nullptr;
-    st = launch_ortho_split<false, true>(sp, sm);
-  }
+  const bool vec = aligned16(g) && ld_g % (g_f32 ? 4 : 8) == 0;
+  const puro::OrthoSplitParams sp{g, ld_g, l.ld_x, (int32_t)n, (int32_t)k, eps, x[0].hi, x[0].lo, diag_r + l.ld_m};
+  if (g_f32)
+    st = vec ? launch_ortho_split<true, true>(sp, sm) : launch_ortho_split<true, false>(sp, sm);
+  else
+    st = vec ? launch_ortho_split<false, true>(sp, sm) : launch_ortho_split<false, false>(sp, sm);
   if (st != PURO_OK) return st;
 
   for (int i = 0; i < steps; ++i) {
+    const OrthoMat &cur = x[i & 1], &next = x[(i + 1) & 1];
     puro::OrthoParams p{};
-    p.norm_part = i == 0 ? part : nullptr;
-    p.eps = eps;
-    st = tall ? launch_ortho_gemm<128, true, true, puro::kOrthoGram>(cur, cur, mm, p, *dev, sm)
-              : launch_ortho_gemm<128, false, false, puro::kOrthoGram>(cur, cur, mm, p, *dev, sm);
+    p.a = a;
+    p.b = b;
+    p.c = c;
+    p.diag = diag;
+    p.diag_r = diag_r;
+    puro::OrthoParams pg = p;
+    pg.passes = (tall ? n : k) <= puro::kOrthoExactK ? 3 : 1;
+    st = tall ? launch_ortho_gemm<128, true, true, puro::kOrthoGram>(cur, cur, mo, pg, *dev, sm)
+              : launch_ortho_gemm<128, false, false, puro::kOrthoGram>(cur, cur, mo, pg, *dev, sm);
     if (st != PURO_OK) return st;
-    puro::OrthoParams pq{};
-    pq.alpha = c;
-    pq.beta = b;
-    pq.diag = a;
-    pq.m_hi = mm.hi;
-    pq.m_lo = mm.lo;
-    pq.ld_m = mm.ld;
-    st = launch_ortho_gemm<128, false, false, puro::kOrthoPoly>(mm, mm, pp, pq, *dev, sm);
+    p.passes = 1;
+    p.src_hi = mo.hi;
+    p.ld_src = mo.ld;
+    st = launch_ortho_gemm<128, false, false, puro::kOrthoPoly>(mo, mo, ro, p, *dev, sm);
     if (st != PURO_OK) return st;
-    Split next = x[(i + 1) & 1];
-    p.last = i == steps - 1;
-    if (p.last) {
+    p.src_hi = cur.hi;
+    p.src_lo = cur.lo;
+    p.ld_src = cur.ld;
+    p.col_diag = tall;
+    OrthoMat d = next;
+    if (i == steps - 1) {
+      p.last = 1;
       p.out = static_cast<__nv_bfloat16*>(out);
       p.ld_out = ld_out;
       p.out_tma = aligned16(out) && ld_out % 8 == 0;
-      next = Split{p.out, nullptr, n, k, ld_out};
+      d.ld = ld_out;
     }
-    st = tall ? launch_ortho_gemm<256, false, false, puro::kOrthoUpdate>(cur, pp, next, p, *dev, sm)
-              : launch_ortho_gemm<256, false, true, puro::kOrthoUpdate>(pp, cur, next, p, *dev, sm);
+    st = tall ? launch_ortho_gemm<256, false, false, puro::kOrthoUpdate>(cur, ro, d, p, *dev, sm)
+              : launch_ortho_gemm<256, false, true, puro::kOrthoUpdate>(ro, cur, d, p, *dev, sm);
     if (st != PURO_OK) return st;
-    cur = next;
   }
   return PURO_OK;
 }

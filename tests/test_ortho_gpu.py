@@ -2,13 +2,14 @@
 
 Errors are relative to the norm of the result.  Its one rounding to BF16 is off
 by at most half a step: between 2^-9 and 2^-8 of a value, evenly spread, so at
-most 2^-8 / sqrt(3) = 2.26e-3 in the mean square.  Between, operands have 16
-significant bits (two BF16 terms, off by at most 2^-17).  A step's polynomial
-sums terms of 3.4 + 4.8 + 2.0 = 10.3 times its result, so its roundings are at
-most 10.3 * 2^-17 of the strongest direction; the inputs here hold a floor of
-at least 1/20 of that direction, so they are at most 20 * 10.3 * 2^-17 =
-1.6e-3 of any direction that counts (and grow no faster than it does).  The
-bound is 2.26e-3 + 1.6e-3 = 3.9e-3.
+most 2^-8 / sqrt(3) = 2.26e-3 in the mean square.  Between, X is
+exact to 22 bits and what enters a product is rounded to FP16 off the diagonal:
+a relative error of at most 2^-11 / sqrt(3) = 2.8e-4 in the mean square.  Five
+steps take three products of two operands each, so 30 independent roundings,
+sqrt(30) * 2.8e-4 = 1.6e-3.  (A step changes the relative error of a direction
+by the factor x p'(x) / p(x), which is 1 for small x and, where x has grown to
+0.7 or more, between -1.7 and 1: later steps do not let earlier errors grow.)
+The bound is the plain sum, 2.26e-3 + 1.6e-3 = 3.9e-3.
 """
 import pytest
 import torch
