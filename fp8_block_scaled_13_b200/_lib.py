@@ -89,8 +89,8 @@ def load() -> ctypes.CDLL:
                                               I, I, I, INT, P]
     F = ctypes.c_float
     codes = [INT, P, I, P, P, I, P, P, I]  # layout, q, ld_q, s, qt, ld_qt, st, bf16, ld_bf16
-    lib.puro_fp8_residual_norm.argtypes = [P, I, P, I, P, P, INT, P, I, INT, INT, F, F, I, I, P, I, P, P, *codes, P]
-    lib.puro_fp8_residual_norm_workspace_bytes.argtypes = [I, I]
+    lib.puro_fp8_residual_norm.argtypes = [P, I, P, I, P, P, INT, P, I, INT, INT, F, F, I, I, P, I, P, P, *codes, P, P]
+    lib.puro_fp8_residual_norm_workspace_bytes.argtypes = [I, I, INT, INT]
     lib.puro_fp8_residual_norm_workspace_bytes.restype = I
     lib.puro_fp8_residual_norm_backward.argtypes = [P, I, P, I, P, I, P, P, I, P, P, P, INT, P, I, INT, INT, F, I, I,
                                                     P, I, P, P, P, I, INT, *codes, P, P]
@@ -161,8 +161,8 @@ def puro_fp8_residual_norm(*args) -> int:
     return load().puro_fp8_residual_norm(*args)
 
 
-def puro_fp8_residual_norm_workspace_bytes(rows, cols) -> int:
-    return load().puro_fp8_residual_norm_workspace_bytes(rows, cols)
+def puro_fp8_residual_norm_workspace_bytes(rows, cols, layout, backward) -> int:
+    return load().puro_fp8_residual_norm_workspace_bytes(rows, cols, layout, backward)
 
 
 def puro_fp8_residual_norm_backward(*args) -> int:

@@ -177,12 +177,14 @@ def residual_norm(x: torch.Tensor, w_pre: torch.Tensor, h: torch.Tensor | None =
         raise ValueError("y is only written with a block output h")
     kind, g_f32, ld_gate = _gate(gate, rows, cols)
     res = _result(out, rows, cols, flag, dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd_post = torch.empty(rows, dtype=torch.float32, device=dev) if w_post is not None else None
+    # one allocation: the workspace (64 words) and the factors
+    buf = torch.empty(64 + (rows if w_post is None else 2 * rows), dtype=torch.float32, device=dev)
+    rstd = buf[64:64 + rows]
+    rstd_post = buf[64 + rows:] if w_post is not None else None
     st = _lib.puro_fp8_residual_norm(
         x.data_ptr(), x.stride(0), _ptr(h), _ld(h), w_pre.data_ptr(), _ptr(w_post), w_f32, _ptr(gate), ld_gate, kind,
         g_f32, scale, eps, rows, cols, _ptr(y), _ld(y), rstd.data_ptr(), _ptr(rstd_post), flag,
-        *_result_args(res, flag), _stream())
+        *_result_args(res, flag), buf.data_ptr(), _stream())
     _check(st, "puro_fp8_residual_norm")
     return ResidualNorm(x if h is None else y, res, rstd, rstd_post)
 
@@ -243,7 +245,8 @@ def residual_norm_backward(dn: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor
         if kind == _lib.PURO_GATE_TOKEN and not dgate.is_contiguous():
             raise ValueError("dgate must be contiguous")
     res = _result(out, rows, cols, flag, dev) if h is not None else None
-    ws = torch.empty(max(_lib.puro_fp8_residual_norm_workspace_bytes(rows, cols), 16), dtype=torch.uint8, device=dev)
+    ws = torch.empty(max(_lib.puro_fp8_residual_norm_workspace_bytes(rows, cols, flag if h is not None else 0, 1), 16),
+                     dtype=torch.uint8, device=dev)
     st = _lib.puro_fp8_residual_norm_backward(
         dn.data_ptr(), dn.stride(0), _ptr(dy), _ld(dy), y.data_ptr(), y.stride(0), rstd.data_ptr(), _ptr(h), _ld(h),
         _ptr(rstd_post), w_pre.data_ptr(), _ptr(w_post), w_f32, _ptr(gate), ld_gate, kind, g_f32, scale, rows, cols,

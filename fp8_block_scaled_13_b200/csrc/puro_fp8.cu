@@ -145,7 +145,7 @@ int launch_status() {
 
 // ------------------------------------------------------------------ quant
 
-template <bool ROW, bool COL, bool BLOCK, bool RSHFL, int STAGES>
+template <bool ROW, bool COL, bool BLOCK, bool RSHFL, int STAGES, bool NORM = false>
 int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, const DeviceInfo& dev,
                      cudaStream_t stream) {
   int st = get_encoder();
@@ -165,7 +165,7 @@ int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, co
     if ((st = make_map_qt(&mqt, p.qt, BLOCK ? p.rows : (p.rows + 15) / 16 * 16, p.cols, p.ld_qt)) != PURO_OK)
       return st;
   }
-  auto kern = puro::quant_kernel<ROW, COL, BLOCK, RSHFL, STAGES>;
+  auto kern = puro::quant_kernel<ROW, COL, BLOCK, RSHFL, STAGES, NORM>;
   constexpr uint32_t smem = puro::quant_smem_bytes<STAGES>();
   // per device, once (threads racing on the first call both set the same value)
   static std::atomic<bool> attr_done[kMaxDevices] = {};
@@ -201,7 +201,7 @@ int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, co
 // per SM there are warps enough to hide the shuffles' latency).  Weights (at
 // most a few thousand tiles) take two stages and the static schedule.  Each
 // form was measured faster in its own range.
-template <bool ROW, bool COL, bool BLOCK>
+template <bool ROW, bool COL, bool BLOCK, bool NORM = false>
 int launch_quant(const void* x, int64_t ld_x, const puro::QuantParams& p, const DeviceInfo& dev,
                  cudaStream_t stream) {
   const bool short_stream = p.tiles <= 8 * 2 * (int64_t)dev.sms;
@@ -219,8 +219,8 @@ int launch_quant(const void* x, int64_t ld_x, const puro::QuantParams& p, const 
   if constexpr (BLOCK) {
     return launch_quant_cfg<ROW, COL, BLOCK, false, 2>(x, ld_x, ps, dev, stream);
   } else {
-    if (short_stream) return launch_quant_cfg<ROW, COL, BLOCK, ROW, 2>(x, ld_x, ps, dev, stream);
-    return launch_quant_cfg<ROW, COL, BLOCK, ROW, 1>(x, ld_x, ps, dev, stream);
+    if (short_stream) return launch_quant_cfg<ROW, COL, BLOCK, ROW, 2, NORM>(x, ld_x, ps, dev, stream);
+    return launch_quant_cfg<ROW, COL, BLOCK, ROW, 1, NORM>(x, ld_x, ps, dev, stream);
   }
 }
 
@@ -838,6 +838,7 @@ int norm_common_args(const void* w_pre, const void* w_post, int w_f32, const voi
   p->gate_kind = h ? gate_kind : PURO_GATE_NONE;
   p->gate_f32 = gate_f32;
   p->scale = scale;
+  p->wide = aligned16(w_pre) && aligned16(p->w_post) && (gate_kind != PURO_GATE_CHANNEL || aligned16(gate));
   return PURO_OK;
 }
 
@@ -850,30 +851,20 @@ int norm_flags(int w_f32, int gate_kind, int gate_f32, int64_t rows, int64_t col
   return PURO_OK;
 }
 
-// Launches `kern` on `grid` CTAs in clusters of `cluster` (1: none).
-template <class Kern>
-int launch_norm_cfg(Kern kern, const puro::NormParams& p, int64_t grid, int threads, uint32_t smem, int cluster,
-                    std::atomic<bool>* attr_done, const DeviceInfo& dev, cudaStream_t stream) {
-  if (!attr_done[dev.index].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return PURO_ERR_CUDA;
-    attr_done[dev.index].store(true, std::memory_order_release);
-  }
+// Launches `kern` on `grid` CTAs; it may start while the kernel before it on
+// the stream still runs.
+template <class Kern, class Params>
+int launch_chained(Kern kern, const Params& p, dim3 grid, int threads, uint32_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
     cudaGetLastError();
     return PURO_ERR_CUDA;
@@ -881,28 +872,81 @@ int launch_norm_cfg(Kern kern, const puro::NormParams& p, int64_t grid, int thre
   return PURO_OK;
 }
 
-template <int MAXT, int RPC, bool COL>
-int launch_norm(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
-  static std::atomic<bool> done[kMaxDevices] = {};
-  const int threads = (p.cols / 8 + 31) / 32 * 32;
-  // Without transposed codes no cluster is needed, and a CTA takes as many
-  // rows (a power of two, so that CTAs never straddle a 128-row block of
-  // scales) as still leave every SM two CTAs.
-  p.rpc = RPC;
-  if (!COL)
-    while (p.rpc > 1 && p.rows < (int64_t)p.rpc * 2 * dev.sms) p.rpc /= 2;
-  const int64_t grid = COL ? (p.rows + 127) / 128 * (128 / RPC) : (p.rows + p.rpc - 1) / p.rpc;
-  return launch_norm_cfg(puro::norm_kernel<MAXT, RPC, COL>, p, grid, threads,
-                         puro::norm_smem_bytes<RPC, COL, false>(p.cols), COL ? 128 / RPC : 1, done, dev, stream);
+// Quantizer parameters of a BF16 tensor [rows, cols] that the kernel before
+// this one leaves, its tile counter included.
+puro::QuantParams quant_params(const puro::CodeOut& o, int64_t rows, int64_t cols, uint32_t* ctr) {
+  puro::QuantParams p{};
+  p.ctr = ctr;
+  p.rows = rows;
+  p.cols = cols;
+  p.q = o.q;
+  p.ld_q = o.ld_q;
+  p.s = o.s;
+  p.s_g4 = o.s_g4;
+  p.qt = o.qt;
+  p.ld_qt = o.ld_qt;
+  p.st = o.st;
+  p.st_g4 = o.st_g4;
+  p.tiles_c = (int32_t)(cols / 128);
+  p.tiles = (int32_t)(p.tiles_c * ((rows + 127) / 128));
+  return p;
 }
 
-template <int MAXT, int RPC, bool COL>
-int launch_norm_backward(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
+// Rows that a CTA of a row pass takes: 32, or fewer, down to `least`, where that
+// would leave an SM without its `resident` CTAs.  (148 SMs: the split, and with
+// it the order in which the backward pass adds its sums over tokens, does not
+// depend on the device's state.)
+constexpr int64_t kNormSms = 148;
+int norm_rpc(int64_t rows, int64_t resident, int least) {
+  int rpc = 32;
+  while (rpc > least && rows < rpc * resident * kNormSms) rpc /= 2;
+  return rpc;
+}
+int norm_backward_rpc(int64_t rows, int64_t cols) {
+  return norm_rpc(rows, cols <= 2048 ? 2 : 1, cols <= 4096 ? 4 : 2);
+}
+
+int64_t norm_backward_parts(int64_t rows, int64_t cols) {
+  const int rpc = norm_backward_rpc(rows, cols);
+  return (rows + rpc - 1) / rpc;
+}
+
+// The workspace: the tile counter of the quantizing pass, the partial column
+// sums and, where transposed codes are asked for, dh in BF16.
+constexpr int64_t kNormCounterBytes = 256;
+int64_t norm_part_bytes(int64_t rows, int64_t cols) {
+  return norm_backward_parts(rows, cols) * 2 * cols * (int64_t)sizeof(float);
+}
+
+template <class Kern>
+int launch_norm_pass(Kern kern, std::atomic<bool>* done, uint32_t max_smem, const puro::NormParams& p, uint32_t smem,
+                     const DeviceInfo& dev, cudaStream_t stream) {
+  if (!done[dev.index].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)max_smem) != cudaSuccess)
+      return PURO_ERR_CUDA;
+    done[dev.index].store(true, std::memory_order_release);
+  }
+  return launch_chained(kern, p, dim3((unsigned)((p.rows + p.rpc - 1) / p.rpc)), (p.cols / 8 + 31) / 32 * 32, smem,
+                        stream);
+}
+
+template <int MAXT, int ROWS>
+int launch_norm_forward(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevices] = {};
+  p.rpc = norm_rpc(p.rows, MAXT == 256 ? 3 : 1, 1);
+  const int threads = (p.cols / 8 + 31) / 32 * 32;
+  const int tensors = 1 + (p.h != nullptr) + (p.gate_kind == PURO_GATE_FULL);
+  return launch_norm_pass(puro::norm_forward_kernel<MAXT, ROWS>, done, puro::norm_pass_smem(ROWS, MAXT, 3), p,
+                          puro::norm_pass_smem(ROWS, threads, tensors), dev, stream);
+}
+
+template <int MAXT, int ROWS>
+int launch_norm_backward(const puro::NormParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices] = {};
   const int threads = (p.cols / 8 + 31) / 32 * 32;
-  p.rpc = RPC;
-  return launch_norm_cfg(puro::norm_backward_kernel<MAXT, RPC, COL>, p, (p.rows + 127) / 128 * (128 / RPC),
-                         threads, puro::norm_smem_bytes<RPC, COL, true>(p.cols), 128 / RPC, done, dev, stream);
+  const int tensors = 2 + (p.dy != nullptr) + (p.h != nullptr) + (p.gate_kind == PURO_GATE_FULL);
+  return launch_norm_pass(puro::norm_backward_kernel<MAXT, ROWS>, done, puro::norm_pass_smem(ROWS, MAXT, 5), p,
+                          puro::norm_pass_smem(ROWS, threads, tensors), dev, stream);
 }
 
 template <bool BWD, bool ROW, bool COL, bool BF>
@@ -973,7 +1017,7 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
                            const void* w_post, int w_f32, const void* gate, int64_t ld_gate, int gate_kind,
                            int gate_f32, float scale, float eps, int64_t rows, int64_t cols, void* y, int64_t ld_y,
                            float* rstd, float* rstd_post, int layout, void* q, int64_t ld_q, void* s, void* qt,
-                           int64_t ld_qt, void* st, void* n, int64_t ld_n, void* stream) {
+                           int64_t ld_qt, void* st, void* n, int64_t ld_n, void* workspace, void* stream) {
   int r;
   if ((r = norm_flags(w_f32, gate_kind, gate_f32, rows, cols, layout)) != PURO_OK) return r;
   if (!(eps > 0.f)) return PURO_ERR_SHAPE;
@@ -990,6 +1034,16 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
   if (!rstd || (p.w_post && !rstd_post)) return PURO_ERR_NULL;
   if (!aligned_to(rstd, 4) || !aligned_to(rstd_post, 4)) return PURO_ERR_ALIGN;
   if ((r = code_out_args(layout, rows, cols, q, ld_q, s, qt, ld_qt, st, n, ld_n, &p.out)) != PURO_OK) return r;
+  // Row-wise codes and BF16 come from the row pass; transposed codes, and the
+  // row-wise ones beside them, from the tile pass over y.
+  const bool col = p.out.qt != nullptr;
+  const puro::CodeOut out = p.out;
+  if (col) {
+    if (!workspace) return PURO_ERR_NULL;
+    if (!aligned16(workspace)) return PURO_ERR_ALIGN;
+    p.ctr = static_cast<uint32_t*>(workspace);
+    p.out = puro::CodeOut{};
+  }
   DeviceInfo* dev = nullptr;
   if ((r = current_device(&dev)) != PURO_OK) return r;
   p.x = static_cast<const __nv_bfloat16*>(x);
@@ -1002,15 +1056,26 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
   p.rstd = rstd;
   p.rstd_post = rstd_post;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
-  const bool col = p.out.qt != nullptr;
-  if (cols <= 2048) return col ? launch_norm<256, 16, true>(p, *dev, sm) : launch_norm<256, 16, false>(p, *dev, sm);
-  if (cols <= 4096) return col ? launch_norm<512, 16, true>(p, *dev, sm) : launch_norm<512, 16, false>(p, *dev, sm);
-  return col ? launch_norm<1024, 8, true>(p, *dev, sm) : launch_norm<1024, 8, false>(p, *dev, sm);
+  r = cols <= 2048   ? launch_norm_forward<256, 4>(p, *dev, sm)
+      : cols <= 4096 ? launch_norm_forward<512, 4>(p, *dev, sm)
+                     : launch_norm_forward<1024, 2>(p, *dev, sm);
+  if (r != PURO_OK || !col) return r;
+  puro::QuantParams qp = quant_params(out, rows, cols, p.ctr);
+  qp.rstd = rstd;
+  qp.w = w_pre;
+  qp.w_f32 = w_f32;
+  qp.w_wide = aligned16(w_pre);
+  const void* src = h ? y : x;
+  const int64_t ld = h ? ld_y : ld_x;
+  return out.q ? launch_quant<true, true, false, true>(src, ld, qp, *dev, sm)
+               : launch_quant<false, true, false, true>(src, ld, qp, *dev, sm);
 }
 
-int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols) {
+int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols, int layout, int backward) {
   if (rows <= 0 || cols <= 0) return 0;
-  return (rows + 127) / 128 * 2 * cols * (int64_t)sizeof(float);
+  const bool col = layout == PURO_COLWISE || layout == PURO_BOTH;
+  if (!backward) return col ? kNormCounterBytes : 0;
+  return kNormCounterBytes + norm_part_bytes(rows, cols) + (col ? rows * cols * 2 : 0);
 }
 
 int puro_fp8_residual_norm_backward(const void* dn, int64_t ld_dn, const void* dy, int64_t ld_dy, const void* y,
@@ -1072,19 +1137,32 @@ int puro_fp8_residual_norm_backward(const void* dn, int64_t ld_dn, const void* d
     p.ld_dx = ld_dx;
     p.dgate = dgate;
     p.ld_dgate = ld_dgate;
-    p.part = static_cast<float*>(workspace);
+    char* ws = static_cast<char*>(workspace);
+    p.part = reinterpret_cast<float*>(ws + kNormCounterBytes);
+    p.rpc = norm_backward_rpc(rows, cols);
     const bool col = p.out.qt != nullptr;
-    if (cols <= 2048)
-      r = col ? launch_norm_backward<256, 16, true>(p, *dev, sm) : launch_norm_backward<256, 16, false>(p, *dev, sm);
-    else if (cols <= 4096)
-      r = col ? launch_norm_backward<512, 16, true>(p, *dev, sm) : launch_norm_backward<512, 16, false>(p, *dev, sm);
-    else
-      r = col ? launch_norm_backward<1024, 8, true>(p, *dev, sm) : launch_norm_backward<1024, 8, false>(p, *dev, sm);
+    const puro::CodeOut out = p.out;
+    if (col) {
+      // dh in BF16 first; the quantizer makes both kinds of codes from it
+      p.ctr = reinterpret_cast<uint32_t*>(ws);
+      p.out = puro::CodeOut{};
+      p.out.bf = reinterpret_cast<__nv_bfloat16*>(ws + kNormCounterBytes + norm_part_bytes(rows, cols));
+      p.out.ld_bf = cols;
+    }
+    r = cols <= 2048   ? launch_norm_backward<256, 2>(p, *dev, sm)
+        : cols <= 4096 ? launch_norm_backward<512, 2>(p, *dev, sm)
+                       : launch_norm_backward<1024, 1>(p, *dev, sm);
     if (r != PURO_OK) return r;
+    if (col) {
+      const puro::QuantParams qp = quant_params(out, rows, cols, p.ctr);
+      r = out.q ? launch_quant<true, true, false>(p.out.bf, cols, qp, *dev, sm)
+                : launch_quant<false, true, false>(p.out.bf, cols, qp, *dev, sm);
+      if (r != PURO_OK) return r;
+    }
   }
   puro::NormColumnParams c{};
-  c.part = static_cast<const float*>(workspace);
-  c.parts = (rows + 127) / 128;
+  c.part = reinterpret_cast<const float*>(static_cast<char*>(workspace) + kNormCounterBytes);
+  c.parts = rows ? norm_backward_parts(rows, cols) : 0;
   c.cols = (int32_t)cols;
   c.w_post = p.w_post;
   c.gate = channel ? gate : nullptr;
@@ -1095,20 +1173,8 @@ int puro_fp8_residual_norm_backward(const void* dn, int64_t ld_dn, const void* d
   c.dw_pre = dw_pre;
   c.dw_post = p.w_post ? dw_post : nullptr;
   c.dgate = channel ? static_cast<float*>(dgate) : nullptr;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(cols / 32));
-  cfg.blockDim = dim3(256);
-  cfg.stream = sm;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, puro::norm_column_kernel, c) != cudaSuccess) {
-    cudaGetLastError();
-    return PURO_ERR_CUDA;
-  }
-  return PURO_OK;
+  return launch_chained(puro::norm_column_kernel, c, dim3((unsigned)(cols / 32), c.dw_post || c.dgate ? 2 : 1), 512, 0,
+                        sm);
 }
 
 int puro_fp8_swiglu(const void* gu, int64_t ld_gu, int64_t rows, int64_t f, int layout, void* q, int64_t ld_q,

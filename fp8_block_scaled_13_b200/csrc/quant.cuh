@@ -45,6 +45,8 @@
 // saturating conversion to E4M3 per value.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 
 namespace puro {
@@ -89,6 +91,11 @@ struct QuantParams {
   // draws ticket tiles-1 knows every other CTA has drawn its last, and sets
   // the counter back to zero.
   uint32_t* ctr;
+  // NORM: the input is multiplied by rstd[row] and w[col] first and rounded to
+  // BF16 again (the RMS norm's output)
+  const float* rstd;
+  const void* w;
+  int32_t w_f32, w_wide;
 };
 
 // Scale exponents of two groups at once.  a2 holds two amax magnitudes (BF16
@@ -241,6 +248,101 @@ __device__ __forceinline__ uint32_t blocked_in_chunk(int r) {
   return static_cast<uint32_t>((r & 31) * 16 + ((r >> 5) & 3) * 4);
 }
 
+// Two FP32 values that one instruction works on (packed FP32 arithmetic, each
+// half rounded as its scalar form rounds).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_both(float v) { return f2_of(v, v); }
+__device__ __forceinline__ float f2_sum(f2 v) {
+  const float2 p = f2_get(v);
+  return p.x + p.y;
+}
+
+// The 8 BF16 values of a 16-byte word as FP32, and back.
+__device__ __forceinline__ void unpack8(const uint4& v, f2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+  const float2 p = f2_get(v);
+  return pack2(p.x, p.y);
+}
+
+__device__ __forceinline__ uint4 pack8(const f2 (&f)[4]) {
+  return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+__device__ __forceinline__ float load_param(const void* p, int32_t f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i]
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// Eight consecutive values of a parameter vector (wide: it starts on a 16-byte
+// boundary; i is a multiple of 8).
+__device__ __forceinline__ void load_param8(const void* p, int32_t f32, int32_t wide, int32_t i, f2 (&v)[4]) {
+  if (wide && f32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = s[0], b = s[1];
+    v[0] = f2_of(a.x, a.y);
+    v[1] = f2_of(a.z, a.w);
+    v[2] = f2_of(b.x, b.y);
+    v[3] = f2_of(b.z, b.w);
+  } else if (wide) {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i), v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f2_of(load_param(p, f32, i + 2 * e), load_param(p, f32, i + 2 * e + 1));
+  }
+}
+
+// n = y r2 w of eight columns, as the row pass and the tile pass both form it.
+__device__ __forceinline__ uint4 normed8(const uint4& y, float r2, const f2 (&w)[4]) {
+  f2 f[4];
+  unpack8(y, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], f2_both(r2)), w[i]);
+  return pack8(f);
+}
+
 // RSHFL marks the row-scale form of activation launches (ROW without BLOCK):
 // the 16 lanes of a row group reduce-scatter the row maxima, one lane per row
 // derives the exponent and the others read 2^-e with shuffles.  (An earlier
@@ -251,7 +353,10 @@ __device__ __forceinline__ uint32_t blocked_in_chunk(int r) {
 // Addressing is kept out of the per-element work: every output pointer is
 // formed once per tile from per-thread constants and advanced by its stride,
 // and the ragged-edge tests are one 32-bit compare against a per-tile count.
-template <bool ROW, bool COL, bool BLOCK, bool RSHFL, int STAGES>
+//
+// NORM: the quantized tensor is the RMS norm of the input, from the factors
+// that a row pass has left (see norm.cuh).
+template <bool ROW, bool COL, bool BLOCK, bool RSHFL, int STAGES, bool NORM = false>
 __global__ void __launch_bounds__(kQThreads, STAGES == 1 ? 3 : 2)
     quant_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_qt,
                  const QuantParams p) {
@@ -346,6 +451,14 @@ __global__ void __launch_bounds__(kQThreads, STAGES == 1 ? 3 : 2)
     const uint8_t* tile = tiles + s * kQTileBytes + (8 * i) * 256 + 16 * j;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = (ok && tr >= 0) ? lds_v4(tile + k * 256) : make_uint4(0, 0, 0, 0);
+    float rs[NORM ? 8 : 1];
+    f2 nw[4];
+    if (NORM && tr >= 0) {
+      const int64_t r = r0 + 8 * i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) rs[NORM ? k : 0] = r + k < p.rows ? p.rstd[r + k] : 0.f;
+      load_param8(p.w, p.w_f32, p.w_wide, c0 + 8 * j, nw);
+    }
     // every thread holds its part: stage s is free again, and every thread
     // has finished the previous tile, its transposed codes included (and if
     // any wait gave up, the whole block stops here together; every thread
@@ -360,6 +473,13 @@ __global__ void __launch_bounds__(kQThreads, STAGES == 1 ? 3 : 2)
       tma_store_3d(&tm_qt, qt_buf + ((it - 1) & 1) * kQtTileBytes, prev_r0, prev_c0 >> 3, 0);
       bulk_commit_group();
       bulk_wait_group_read<1>();
+    }
+
+    if (NORM) {
+      // rows past the end stay zero, whatever the weights
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = r0 + 8 * i + k < p.rows ? normed8(v[k], rs[NORM ? k : 0], nw) : make_uint4(0, 0, 0, 0);
     }
 
     // ---- magnitudes: per-row amax of this thread's 8 columns (two rows per

@@ -295,7 +295,7 @@ PURO_API int puro_fp8_gemm_dgrad_wgrad(const void* qdy, int64_t ld_qdy, const vo
 
 /*
  * puro_fp8_residual_norm -- the norms around a block, its gate and residual
- * sum, and the FP8 quantization of the next linear layer's input, in one pass.
+ * sum, and the FP8 quantization of the next linear layer's input.
  * (The pages keep the hidden and residual flow and the norms in BF16 around
  * E4M3 linear layers: paperlayer.ai Appendix C.)
  *   hh = h * r1[token],  r1 = rsqrt(mean(h^2) + eps)  (w_post NULL: hh = h)
@@ -311,6 +311,7 @@ PURO_API int puro_fp8_gemm_dgrad_wgrad(const void* qdy, int64_t ld_qdy, const vo
  *             selects FP32 for the other two kinds.
  * y         : BF16 [rows, cols], written; may be x (or h) itself.
  * rstd, rstd_post : FP32 [rows], r2 and (with w_post) r1, for the backward pass.
+ * workspace : see below; may be NULL where its size is 0.
  * cols % 128 == 0, cols <= 8192; any rows >= 0; eps > 0 (PURO_ERR_SHAPE).
  */
 PURO_API int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t ld_h,
@@ -319,11 +320,14 @@ PURO_API int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, 
                                     float scale, float eps, int64_t rows, int64_t cols,
                                     void* y, int64_t ld_y, float* rstd, float* rstd_post, int layout,
                                     void* q, int64_t ld_q, void* s, void* qt, int64_t ld_qt, void* st,
-                                    void* n, int64_t ld_n, void* stream);
+                                    void* n, int64_t ld_n, void* workspace, void* stream);
 
-/* Bytes of the workspace of puro_fp8_residual_norm_backward (16-byte aligned;
- * its contents before and after a call mean nothing); 0 for an empty input. */
-PURO_API int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols);
+/* Bytes of the workspace (16-byte aligned, contents don't matter) of
+ * puro_fp8_residual_norm (backward = 0: 0 or 256 bytes) and of
+ * puro_fp8_residual_norm_backward (backward = 1), for outputs in `layout`
+ * (0: backward without h).  Calls that may run at the same time need distinct
+ * ones. */
+PURO_API int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols, int layout, int backward);
 
 /*
  * puro_fp8_residual_norm_backward -- gradients of puro_fp8_residual_norm, from

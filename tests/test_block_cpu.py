@@ -85,7 +85,7 @@ def test_swiglu_backward_formula_against_autograd_and_differences():
 def _norm(**over):
     a = dict(x=A, ld_x=256, h=A, ld_h=256, w_pre=A, w_post=A, w_f32=0, gate=A, ld_gate=256, kind=3, gate_f32=0,
              scale=1.0, eps=1e-6, rows=64, cols=256, y=A, ld_y=256, rstd=A, rstd_post=A, layout=3, q=A, ld_q=256, s=A,
-             qt=A, ld_qt=64, st=A, n=None, ld_n=0)
+             qt=A, ld_qt=64, st=A, n=None, ld_n=0, workspace=A)
     assert set(over) <= set(a)
     a.update(over)
     return tuple(a.values())
@@ -99,6 +99,7 @@ def _norm(**over):
     (dict(x=None), -1), (dict(w_pre=None), -1), (dict(y=None), -1), (dict(rstd=None), -1), (dict(rstd_post=None), -1),
     (dict(gate=None), -1), (dict(q=None), -1), (dict(s=None), -1), (dict(qt=None), -1), (dict(st=None), -1),
     (dict(layout=4), -1),                                        # BF16 result without its buffer
+    (dict(workspace=None), -1), (dict(layout=2, workspace=None), -1), (dict(workspace=A + 8), -2),
     (dict(ld_x=128), -3), (dict(ld_h=128), -3), (dict(ld_y=128), -3), (dict(ld_gate=128), -3),
     (dict(ld_qt=48), -3), (dict(layout=4, n=A, ld_n=128), -3),
     (dict(x=A + 2), -2), (dict(h=A + 8), -2), (dict(ld_x=260), -2), (dict(w_pre=A + 1), -2), (dict(rstd=A + 2), -2),
@@ -157,8 +158,20 @@ def test_empty_inputs_are_no_ops(lib):
     assert lib.puro_fp8_residual_norm_backward(*_norm_bwd(cols=0, dn=None, dw_pre=None), None) == 0
     assert lib.puro_fp8_swiglu(None, 0, 0, 256, 3, None, 0, *none[:2], 0, *none[:2], 0, None) == 0
     assert lib.puro_fp8_swiglu(None, 0, 5, 0, 3, None, 0, *none[:2], 0, *none[:2], 0, None) == 0
-    assert lib.puro_fp8_residual_norm_workspace_bytes(0, 256) == 0
-    assert lib.puro_fp8_residual_norm_workspace_bytes(129, 256) == 2 * 2 * 256 * 4
+
+
+def test_workspace_sizes(lib):
+    size = lib.puro_fp8_residual_norm_workspace_bytes
+    for layout in (0, 1, 2, 3, 4):
+        assert size(0, 256, layout, 0) == size(0, 256, layout, 1) == size(5, 0, layout, 1) == 0
+    assert [size(129, 256, layout, 0) for layout in (1, 2, 3, 4)] == [0, 256, 256, 0]
+    for rows in (1, 4, 5, 129, 1000, 9471, 9472, 32768, 1 << 24):
+        for cols in (128, 2048, 4096, 8192):
+            sums = size(rows, cols, 1, 1)
+            assert sums == size(rows, cols, 0, 1) == size(rows, cols, 4, 1)
+            parts = (sums - 256) // (2 * cols * 4)
+            assert -(-rows // 32) <= parts <= max(-(-rows // 32), 4 * 148) + 1 and parts * 2 * cols * 4 + 256 == sums
+            assert size(rows, cols, 2, 1) == size(rows, cols, 3, 1) == sums + rows * cols * 2
 
 
 # ------------------------------------------------------------------ refusals of the wrappers
