@@ -8,11 +8,19 @@
 // for the BF16 tensor.
 //
 // Bound by HBM: 4 bytes read and 2 written per element forward, 6 and 4
-// backward.  A CTA of 256 threads takes one 128 x 128 tile -- the unit in
+// backward.  A CTA of 256 threads works on 128 x 128 tiles -- the unit in
 // which both groupings (1x128 along a row, 128x1 along a column) close, so
 // nothing is exchanged between CTAs -- and thread (i, j) holds rows 8i..8i+7,
 // columns 8j..8j+7, as the quantizer's threads do.  Backward, one CTA writes
-// the tile of dg and that of du from one read of the three inputs.
+// the tile of dg and that of du from one read of the three inputs.  While a
+// tile is encoded, TMA brings the next one into the stage that its values have
+// left: two CTAs per SM keep 128 KB (backward 192 KB) in flight.  The grid has
+// one CTA per tile, and a CTA that is done takes over the tile of one that has
+// not been launched yet (cluster launch control), so that SMs that stream
+// faster take more tiles without a counter to set up.  (One tile per CTA,
+// loaded into registers, left the memory idle while it was encoded:
+// 32768 x 6144 took @OLDF@ us, 16384 x 6144 backward @OLDB@ us, against @NEWF@
+// and @NEWB@.)
 #pragma once
 
 #include "common.cuh"
@@ -25,24 +33,49 @@ struct GatedParams {
   int64_t rows;
   int32_t f;                    // columns of g, of u and of da
   int32_t tiles_c;              // f / 128
-  const __nv_bfloat16* gu;      // [rows][2f]
-  int64_t ld_gu;
-  const __nv_bfloat16* da;      // backward: [rows][f]
-  int64_t ld_da;
   CodeOut out;                  // forward [rows][f], backward [rows][2f]
 };
 
-constexpr uint32_t kGatedSmemBytes = kQtTileBytes + 8 * 64 * 4 + 128 * 4 + 1024;
+// The input stage, the transposed codes' staging tile (1024-byte aligned; the
+// column maxima live in it before), the column scales, two barriers, the
+// answer of the launch control and two words.
+template <bool BWD>
+constexpr uint32_t gated_smem_bytes() {
+  return (BWD ? 3 : 2) * kQTileBytes + kQtTileBytes + 128 * 4 + 16 + 16 + 16;
+}
+
+// Asks for the tile of a CTA that has not been launched yet; the answer
+// completes 16 bytes on the barrier.
+__device__ __forceinline__ void request_tile(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The tile of the answer, or -1.
+__device__ __forceinline__ int32_t requested_tile(const void* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got ? (int32_t)x : -1;
+}
 
 // Quantizes the 128 x 128 tile (tr, tc) that the block holds in v (rows past
 // the end zero) and writes its codes and scales, or stores it as BF16.
-// Shared memory: qt_s 16 KB (1024-byte aligned), col_part [8][16][4],
-// col_scale [128]; free for reuse after the caller's next barrier, qt_s once
-// the tensor store has read it.
 template <bool ROW, bool COL, bool BF>
 __device__ __forceinline__ void emit_tile(const uint4 (&v)[8], const CodeOut& o, const CUtensorMap* tm_qt,
                                           int64_t rows, int32_t tr, int32_t tc, uint8_t* qt_s,
-                                          uint32_t* col_part, float* col_scale) {
+                                          float* col_scale) {
   const int tid = threadIdx.x, i = tid >> 4, j = tid & 15, warp = tid >> 5;
   const int64_t r0 = (int64_t)tr * 128 + 8 * i;
   const int32_t c0 = tc * 128 + 8 * j;
@@ -53,7 +86,27 @@ __device__ __forceinline__ void emit_tile(const uint4 (&v)[8], const CodeOut& o,
     for (int k = 0; k < 8; ++k, d += o.ld_bf)
       if (k < nrow) *reinterpret_cast<uint4*>(d) = v[k];
   }
+  if (ROW) {
+    uint32_t rowmax[4];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const uint4 &x = v[k], &y = v[k + 1];
+      const uint32_t a = amax2(amax2(x.x, x.y), amax2(x.z, x.w)), b = amax2(amax2(y.x, y.y), amax2(y.z, y.w));
+      rowmax[k >> 1] = amax2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632)) & 0x7FFF7FFFu;
+    }
+    uint8_t byte;
+    const float s_mine = share_row_scales(rowmax, j, &byte);
+    if ((j & 1) == 0)
+      o.s[((int64_t)tr * o.s_g4 + (tc >> 2)) * 512 + (tc & 3) + blocked_in_chunk(8 * i + (j >> 1))] = byte;
+    uint8_t* q = o.q + r0 * o.ld_q + c0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k, q += o.ld_q) {
+      const uint2 c = encode_row8(v[k], bf16_bits(__shfl_sync(0xFFFFFFFFu, s_mine, (tid & 16) + 2 * k)));
+      if (k < nrow) *reinterpret_cast<uint2*>(q) = c;
+    }
+  }
   if (COL) {
+    uint32_t* col_part = reinterpret_cast<uint32_t*>(qt_s);  // [8 warps][16][4]
     uint32_t cm[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
     for (int k = 1; k < 8; ++k) {
@@ -67,6 +120,9 @@ __device__ __forceinline__ void emit_tile(const uint4 (&v)[8], const CodeOut& o,
       cm[q] &= 0x7FFF7FFFu;
       cm[q] = __vmaxu2(cm[q], __shfl_xor_sync(0xFFFFFFFFu, cm[q], 16));
     }
+    // the tensor store before has read the staging tile
+    if (tid == 0) bulk_wait_group_read<0>();
+    __syncthreads();
     if ((tid & 16) == 0)
       *reinterpret_cast<uint4*>(&col_part[(warp * 16 + j) * 4]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
     __syncthreads();
@@ -81,30 +137,7 @@ __device__ __forceinline__ void emit_tile(const uint4 (&v)[8], const CodeOut& o,
       s[16] = static_cast<uint8_t>(b2 >> 16);
       *reinterpret_cast<float2*>(&col_scale[2 * tid]) = make_float2(scale_lo(k2), scale_hi(k2));
     }
-  }
-  if (ROW) {
-    uint8_t* q = o.q + r0 * o.ld_q + c0;
-    uint8_t* s = o.s + ((int64_t)tr * o.s_g4 + (tc >> 2)) * 512 + (tc & 3);
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const uint4 &x = v[k], &y = v[k + 1];
-      const uint32_t a = amax2(amax2(x.x, x.y), amax2(x.z, x.w)), b = amax2(amax2(y.x, y.y), amax2(y.z, y.w));
-      uint32_t m = amax2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632)) & 0x7FFF7FFFu;
-#pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-      const uint32_t k2 = scale_k2(m);
-      if (j == k) {
-        const uint32_t bytes = scale_bytes2(m, k2);
-        s[blocked_in_chunk(8 * i + k)] = static_cast<uint8_t>(bytes);
-        s[blocked_in_chunk(8 * i + k + 1)] = static_cast<uint8_t>(bytes >> 16);
-      }
-      if (k < nrow) *reinterpret_cast<uint2*>(q) = encode_row8(x, bf16_bits(scale_lo(k2)));
-      if (k + 1 < nrow) *reinterpret_cast<uint2*>(q + o.ld_q) = encode_row8(y, bf16_bits(scale_hi(k2)));
-      q += 2 * o.ld_q;
-    }
-  }
-  if (COL) {
-    __syncthreads();  // column scales published
+    __syncthreads();  // column scales published, maxima read
     const float4 a = *reinterpret_cast<const float4*>(&col_scale[8 * j]);
     const float4 b = *reinterpret_cast<const float4*>(&col_scale[8 * j + 4]);
     // staging layout of the tensor store: transposed row 8j + l at staging row
@@ -127,68 +160,109 @@ __device__ __forceinline__ void emit_tile(const uint4 (&v)[8], const CodeOut& o,
   }
 }
 
-// sigmoid(g); exp(-g) = inf for very negative g gives 0.
-__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// sigmoid(g) of two values; exp(-g) = inf for very negative g gives 0.
+__device__ __forceinline__ f2 sigmoid2(f2 g) {
+  const float2 v = f2_get(g);
+  return f2_of(__fdividef(1.f, 1.f + __expf(-v.x)), __fdividef(1.f, 1.f + __expf(-v.y)));
+}
 
 template <bool BWD, bool ROW, bool COL, bool BF>
-__global__ void __launch_bounds__(256, 2) gated_kernel(const __grid_constant__ CUtensorMap tm_qt, const GatedParams p) {
-  extern __shared__ uint8_t gsmem_raw[];
-  uint8_t* qt_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint32_t* col_part = reinterpret_cast<uint32_t*>(qt_s + kQtTileBytes);
-  float* col_scale = reinterpret_cast<float*>(col_part + 8 * 64);
+__global__ void __launch_bounds__(256, 2)
+    gated_kernel(const __grid_constant__ CUtensorMap tm_gu, const __grid_constant__ CUtensorMap tm_da,
+                 const __grid_constant__ CUtensorMap tm_qt, const GatedParams p) {
+  constexpr uint32_t kTensors = BWD ? 3 : 2;
+  extern __shared__ __align__(1024) uint8_t gsmem[];
+  uint8_t* stage = gsmem;                                   // g, u, da: [128][128] BF16 each
+  uint8_t* qt_s = gsmem + kTensors * kQTileBytes;
+  float* col_scale = reinterpret_cast<float*>(qt_s + kQtTileBytes);
+  uint8_t* answer = reinterpret_cast<uint8_t*>(col_scale + 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(answer + 16);
+  uint64_t* asked = full + 1;
+  volatile int32_t* next_tile = reinterpret_cast<volatile int32_t*>(full + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + 2) + 1;
   const int tid = threadIdx.x, i = tid >> 4, j = tid & 15;
-  if (COL && tid == 0) prefetch_tmap(&tm_qt);
-  const int32_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
-  const int64_t r0 = (int64_t)tr * 128 + 8 * i;
-  const int32_t nrow = (int32_t)(p.rows - r0 < 8 ? p.rows - r0 : 8);
-  const __nv_bfloat16* gp = p.gu + r0 * p.ld_gu + tc * 128 + 8 * j;
+  if (tid == 0) {
+    mbar_init(full, 1);
+    mbar_init(asked, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_gu);
+    if (BWD) prefetch_tmap(&tm_da);
+    if (COL) prefetch_tmap(&tm_qt);
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 g[8], u[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    g[k] = k < nrow ? ldg_stream(gp + k * p.ld_gu) : zero;
-    u[k] = k < nrow ? ldg_stream(gp + k * p.ld_gu + p.f) : zero;
-  }
-  if (!BWD) {
+
+  // thread 0: the loads of a tile, and the request for the one after it
+  auto load = [&](int32_t t) {
+    const int32_t r = t / p.tiles_c, c = t - r * p.tiles_c;
+    mbar_arrive_expect_tx(full, kTensors * kQTileBytes);
+    tma_load_2d<1>(stage, &tm_gu, c * 128, r * 128, smem_u32(full));
+    tma_load_2d<1>(stage + kQTileBytes, &tm_gu, p.f + c * 128, r * 128, smem_u32(full));
+    if (BWD) tma_load_2d<1>(stage + 2 * kQTileBytes, &tm_da, c * 128, r * 128, smem_u32(full));
+    mbar_arrive_expect_tx(asked, 16);
+    request_tile(answer, asked);
+  };
+  int32_t tile = (int32_t)blockIdx.x;
+  if (tid == 0) load(tile);
+
+  for (uint32_t it = 0;; ++it) {
+    const bool ok = mbar_wait(full, it & 1, abort_flag);
+    const int32_t tr = tile / p.tiles_c, tc = tile - tr * p.tiles_c;
+    // this thread's 8 rows x 8 columns; rows past the end came as zeros and give zeros
+    const uint8_t* src = stage + (8 * i) * 256 + 16 * j;
+    uint4 v[8], w[BWD ? 8 : 1];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float a[8], b[8];
-      unpack8(g[k], a);
-      unpack8(u[k], b);
+      f2 g[4], u[4];
+      unpack8(lds_v4(src + k * 256), g);
+      unpack8(lds_v4(src + kQTileBytes + k * 256), u);
+      if (!BWD) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = a[e] * sigmoid_f(a[e]) * b[e];
-      g[k] = pack8(a);
-    }
-    emit_tile<ROW, COL, BF>(g, p.out, &tm_qt, p.rows, tr, tc, qt_s, col_part, col_scale);
-  } else {
-    const __nv_bfloat16* dp = p.da + r0 * p.ld_da + tc * 128 + 8 * j;
+        for (int e = 0; e < 4; ++e) g[e] = mul2(mul2(g[e], sigmoid2(g[e])), u[e]);
+      } else {
+        f2 d[4];
+        unpack8(lds_v4(src + 2 * kQTileBytes + k * 256), d);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint4 dv = k < nrow ? ldg_stream(dp + k * p.ld_da) : zero;
-      float a[8], b[8], d[8];
-      unpack8(g[k], a);
-      unpack8(u[k], b);
-      unpack8(dv, d);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float s = sigmoid_f(a[e]);
-        const float ds = d[e] * s;
-        d[e] = ds * a[e];                                  // du
-        a[e] = ds * b[e] * fmaf(a[e], 1.f - s, 1.f);       // dg
+        for (int e = 0; e < 4; ++e) {
+          const f2 s = sigmoid2(g[e]), ds = mul2(d[e], s), one = f2_both(1.f);
+          d[e] = mul2(ds, g[e]);                                                           // du
+          g[e] = mul2(mul2(ds, u[e]), fma2(g[e], fma2(s, f2_both(-1.f), one), one));       // dg
+        }
+        w[BWD ? k : 0] = pack8(d);
       }
-      g[k] = pack8(a);
-      u[k] = pack8(d);
+      v[k] = pack8(g);
+      // (keeps the compiler from loading all rows at once, which spills)
+      if (BWD) asm volatile("" ::: "memory");
     }
-    emit_tile<ROW, COL, BF>(g, p.out, &tm_qt, p.rows, tr, tc, qt_s, col_part, col_scale);
-    if (COL) {
-      if (tid == 0) bulk_wait_group_read<0>();
-      __syncthreads();
+    // every thread has read the stage; if any wait gave up, all stop here
+    if (__syncthreads_or(!ok)) break;
+    if (tid == 0) {
+      int32_t next = -1;
+      if (mbar_wait(asked, it & 1, abort_flag)) next = requested_tile(answer);
+      if (next >= 0) {
+        fence_proxy_async_smem();  // the stage's and the answer's reads come before their next writes
+        load(next);
+      }
+      *next_tile = next;
     }
-    emit_tile<ROW, COL, BF>(u, p.out, &tm_qt, p.rows, tr, tc + p.tiles_c, qt_s, col_part, col_scale);
+    emit_tile<ROW, COL, BF>(v, p.out, &tm_qt, p.rows, tr, tc, qt_s, col_scale);
+    if constexpr (BWD) emit_tile<ROW, COL, BF>(w, p.out, &tm_qt, p.rows, tr, tc + p.tiles_c, qt_s, col_scale);
+    if (!COL) __syncthreads();  // next_tile is published (the tile's other barriers do it otherwise)
+    tile = *next_tile;
+    if (tile < 0) break;
   }
   if (COL && tid == 0) bulk_wait_group<0>();
+  // Every copy and request was waited for above, unless a wait gave up; then
+  // let those in flight land (bounded) before the block exits.
+  if (tid == 0 && *abort_flag) {
+    for (uint32_t phase = 0; phase < 2; ++phase) {
+      volatile int no_abort = 0;
+      mbar_wait(full, phase, &no_abort, 100000000ull);
+      mbar_wait(asked, phase, &no_abort, 100000000ull);
+    }
+  }
 }
 
 }  // namespace puro

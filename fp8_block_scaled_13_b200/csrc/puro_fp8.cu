@@ -137,6 +137,19 @@ int make_map_qt(CUtensorMap* m, void* qt, int64_t qt_cols, int64_t cols, int64_t
   return r == CUDA_SUCCESS ? PURO_OK : PURO_ERR_CUDA;
 }
 
+// [outer, inner] 16-bit matrix, boxes of box_inner x box_outer elements.
+int make_map_16(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, uint32_t box_inner,
+                uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PURO_OK : PURO_ERR_CUDA;
+}
+
 int64_t g4_of(int64_t groups) { return (groups + 3) / 4; }
 
 int launch_status() {
@@ -150,16 +163,8 @@ int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, co
                      cudaStream_t stream) {
   int st = get_encoder();
   if (st != PURO_OK) return st;
-  // BF16 input as a 2-D tensor of 16-bit elements {cols, rows}, 128 x 128 boxes
   CUtensorMap m;
-  cuuint64_t dims[2] = {(cuuint64_t)p.cols, (cuuint64_t)p.rows};
-  cuuint64_t strides[1] = {(cuuint64_t)ld_x * 2};
-  cuuint32_t box[2] = {128, 128};
-  cuuint32_t estr[2] = {1, 1};
-  if (g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(x), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return PURO_ERR_CUDA;
+  if ((st = make_map_16(&m, x, p.cols, p.rows, ld_x, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) != PURO_OK) return st;
   CUtensorMap mqt = m;
   if (COL) {
     if ((st = make_map_qt(&mqt, p.qt, BLOCK ? p.rows : (p.rows + 15) / 16 * 16, p.cols, p.ld_qt)) != PURO_OK)
@@ -950,15 +955,27 @@ int launch_norm_backward(const puro::NormParams& p, const DeviceInfo& dev, cudaS
 }
 
 template <bool BWD, bool ROW, bool COL, bool BF>
-int launch_gated_cfg(const puro::GatedParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  CUtensorMap m;
-  memset(&m, 0, sizeof(m));
-  if (COL) {
-    int st;
-    if ((st = get_encoder()) != PURO_OK) return st;
-    if ((st = make_map_qt(&m, p.out.qt, (p.rows + 15) / 16 * 16, (BWD ? 2 : 1) * (int64_t)p.f, p.out.ld_qt)) !=
-        PURO_OK)
-      return st;
+int launch_gated_cfg(const puro::GatedParams& p, const void* gu, int64_t ld_gu, const void* da, int64_t ld_da,
+                     const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap mgu, mda, mqt;
+  int st;
+  if ((st = get_encoder()) != PURO_OK) return st;
+  if ((st = make_map_16(&mgu, gu, 2 * (int64_t)p.f, p.rows, ld_gu, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) != PURO_OK)
+    return st;
+  mda = mqt = mgu;
+  if (BWD &&
+      (st = make_map_16(&mda, da, p.f, p.rows, ld_da, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) != PURO_OK)
+    return st;
+  if (COL &&
+      (st = make_map_qt(&mqt, p.out.qt, (p.rows + 15) / 16 * 16, (BWD ? 2 : 1) * (int64_t)p.f, p.out.ld_qt)) != PURO_OK)
+    return st;
+  auto kern = puro::gated_kernel<BWD, ROW, COL, BF>;
+  constexpr uint32_t smem = puro::gated_smem_bytes<BWD>();
+  static std::atomic<bool> done[kMaxDevices] = {};
+  if (!done[dev.index].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return PURO_ERR_CUDA;
+    done[dev.index].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -966,11 +983,11 @@ int launch_gated_cfg(const puro::GatedParams& p, const DeviceInfo& dev, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)((p.rows + 127) / 128 * p.tiles_c));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = COL ? puro::kGatedSmemBytes : 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, puro::gated_kernel<BWD, ROW, COL, BF>, m, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, mgu, mda, mqt, p) != cudaSuccess) {
     cudaGetLastError();
     return PURO_ERR_CUDA;
   }
@@ -996,16 +1013,12 @@ int gated(const void* da, int64_t ld_da, const void* gu, int64_t ld_gu, int64_t 
   p.rows = rows;
   p.f = (int32_t)f;
   p.tiles_c = (int32_t)(f / 128);
-  p.gu = static_cast<const __nv_bfloat16*>(gu);
-  p.ld_gu = ld_gu;
-  p.da = static_cast<const __nv_bfloat16*>(da);
-  p.ld_da = ld_da;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   switch (layout) {
-    case PURO_ROWWISE: return launch_gated_cfg<BWD, true, false, false>(p, *dev, sm);
-    case PURO_COLWISE: return launch_gated_cfg<BWD, false, true, false>(p, *dev, sm);
-    case PURO_BOTH: return launch_gated_cfg<BWD, true, true, false>(p, *dev, sm);
-    default: return launch_gated_cfg<BWD, false, false, true>(p, *dev, sm);
+    case PURO_ROWWISE: return launch_gated_cfg<BWD, true, false, false>(p, gu, ld_gu, da, ld_da, *dev, sm);
+    case PURO_COLWISE: return launch_gated_cfg<BWD, false, true, false>(p, gu, ld_gu, da, ld_da, *dev, sm);
+    case PURO_BOTH: return launch_gated_cfg<BWD, true, true, false>(p, gu, ld_gu, da, ld_da, *dev, sm);
+    default: return launch_gated_cfg<BWD, false, false, true>(p, gu, ld_gu, da, ld_da, *dev, sm);
   }
 }
 
@@ -1221,19 +1234,6 @@ OrthoLayout ortho_layout(int64_t n, int64_t k) {
   // two X (read and written in turn) as hi and lo; O and O'; D and D'; the norm's partial sums
   l.bytes = (4 * l.x_elems + 2 * l.m_elems) * 2 + (2 * l.ld_m + puro::kOrthoNormBlocks) * (int64_t)sizeof(float);
   return l;
-}
-
-// [outer, inner] 16-bit matrix, boxes of box_inner x box_outer elements.
-int make_map_16(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, uint32_t box_inner,
-                uint32_t box_outer, CUtensorMapSwizzle swizzle) {
-  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? PURO_OK : PURO_ERR_CUDA;
 }
 
 // One product D[i, j] = sum_k A[i, k] B[j, k] of the iteration; AMN / BMN: the

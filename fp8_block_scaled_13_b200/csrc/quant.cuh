@@ -343,6 +343,28 @@ __device__ __forceinline__ uint4 normed8(const uint4& y, float r2, const f2 (&w)
   return pack8(f);
 }
 
+// Reduce-scatter of the magnitudes of eight rows (a row pair per word) over the
+// 16 lanes that hold a row group (lane bits b3 b2 b1 b0 = j): at distance 8 a
+// lane keeps the pair of words for rows 4*b3.. and sends the other pair, at
+// distance 4 it keeps the word for rows 4*b3 + 2*b2 + {0, 1}, then distances 2
+// and 1 finish that word.  Lane j then holds row j >> 1 in half b1 and derives
+// its exponent: 2^-e is returned, the scale byte goes to *byte (even lanes store
+// it, and row k's 2^-e is read from lane 2k).
+__device__ __forceinline__ float share_row_scales(const uint32_t (&rowmax)[4], int j, uint8_t* byte) {
+  const bool b3 = (j >> 3) & 1, b2 = (j >> 2) & 1, b1 = (j >> 1) & 1;
+  uint32_t k0 = b3 ? rowmax[2] : rowmax[0], k1 = b3 ? rowmax[3] : rowmax[1];
+  const uint32_t s0 = b3 ? rowmax[0] : rowmax[2], s1 = b3 ? rowmax[1] : rowmax[3];
+  k0 = __vmaxu2(k0, __shfl_xor_sync(0xFFFFFFFFu, s0, 8));
+  k1 = __vmaxu2(k1, __shfl_xor_sync(0xFFFFFFFFu, s1, 8));
+  uint32_t w = b2 ? k1 : k0;
+  w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, b2 ? k0 : k1, 4));
+  w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
+  w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
+  const uint32_t k2 = scale_k2(w), bytes = scale_bytes2(w, k2);
+  *byte = static_cast<uint8_t>(b1 ? (bytes >> 16) : bytes);
+  return b1 ? scale_hi(k2) : scale_lo(k2);
+}
+
 // RSHFL marks the row-scale form of activation launches (ROW without BLOCK):
 // the 16 lanes of a row group reduce-scatter the row maxima, one lane per row
 // derives the exponent and the others read 2^-e with shuffles.  (An earlier
@@ -564,28 +586,9 @@ __global__ void __launch_bounds__(kQThreads, STAGES == 1 ? 3 : 2)
       const int32_t nrow = (int32_t)(p.rows - r0) - 8 * i;  // rows of the block that exist
       constexpr bool kRowScatter = ROW && !BLOCK && RSHFL;
       if (kRowScatter) {
-        // Reduce-scatter of the four row-pair words over the 16 lanes (lane
-        // bits b3 b2 b1 b0 = j): at distance 8 a lane keeps the pair of words
-        // for rows 4*b3.. and sends the other pair, at distance 4 it keeps the
-        // word for rows 4*b3 + 2*b2 + {0, 1}, then distances 2 and 1 finish
-        // that word.  Lane j then holds row j >> 1 in half b1 and derives its
-        // exponent; even lanes store the scale byte, and row k's 2^-e is read
-        // from lane 2k.
-        const bool b3 = (j >> 3) & 1, b2 = (j >> 2) & 1, b1 = (j >> 1) & 1;
-        uint32_t k0 = b3 ? rowmax[2] : rowmax[0], k1 = b3 ? rowmax[3] : rowmax[1];
-        const uint32_t s0 = b3 ? rowmax[0] : rowmax[2], s1 = b3 ? rowmax[1] : rowmax[3];
-        k0 = __vmaxu2(k0, __shfl_xor_sync(0xFFFFFFFFu, s0, 8));
-        k1 = __vmaxu2(k1, __shfl_xor_sync(0xFFFFFFFFu, s1, 8));
-        uint32_t w = b2 ? k1 : k0;
-        w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, b2 ? k0 : k1, 4));
-        w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
-        w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
-        const uint32_t k2 = scale_k2(w);
-        const uint32_t bytes = scale_bytes2(w, k2);
-        if ((j & 1) == 0)
-          p.s[((int64_t)tr * p.s_g4 + (tc >> 2)) * 512 + (tc & 3) + s_half_chunk] =
-              static_cast<uint8_t>(b1 ? (bytes >> 16) : bytes);
-        const float s_mine = b1 ? scale_hi(k2) : scale_lo(k2);
+        uint8_t byte;
+        const float s_mine = share_row_scales(rowmax, j, &byte);
+        if ((j & 1) == 0) p.s[((int64_t)tr * p.s_g4 + (tc >> 2)) * 512 + (tc & 3) + s_half_chunk] = byte;
         const int lane16 = tid & 16;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
