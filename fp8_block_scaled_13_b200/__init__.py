@@ -18,12 +18,12 @@ _MUON = ("orthogonalize",)
 
 def __getattr__(name):
     if name in _API:
-        from . import linear
-        return getattr(linear, name)
-    if name in _BLOCK:
-        from . import block
-        return getattr(block, name)
-    if name in _MUON:
-        from . import muon
-        return getattr(muon, name)
-    raise AttributeError(name)
+        from . import linear as module
+    elif name in _BLOCK:
+        from . import block as module
+    elif name in _MUON:
+        from . import muon as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # the next access finds it directly
+    return value

@@ -9,6 +9,7 @@ the current stream go to libpuro_fp8.so, and a non-zero status is raised.
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -47,6 +48,14 @@ def _ld(t):
     return t.stride(0) if t is not None else 0
 
 
+def _bf16(t, shape, name):
+    """A row-major BF16 matrix of `shape`, checked: its address and row stride."""
+    stride = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda or stride[1] != 1:
+        _check_tensor(t, shape, (torch.bfloat16,), name)  # (an empty matrix may have any strides)
+    return t.data_ptr(), stride[0]
+
+
 def _layout_flag(layout):
     flag = _OUT_LAYOUTS.get(layout) if isinstance(layout, str) else None
     if flag is None:
@@ -54,15 +63,36 @@ def _layout_flag(layout):
     return flag
 
 
+def _codes(t, rows, cols, name, what, padded=False):
+    """A caller's buffer of codes, checked: its address and row stride."""
+    if t is None:
+        raise ValueError("out has no %s" % what)
+    stride, shape = t.stride(), t.shape
+    if (t.dtype is not torch.uint8 or len(shape) != 2 or shape[0] != rows or not t.is_cuda or stride[1] != 1
+            or (shape[1] < cols if padded else shape[1] != cols)):
+        _check_tensor(t, (rows, cols), (torch.uint8,), name, min_cols=padded)
+    return t.data_ptr(), stride[0]
+
+
+def _scales(t, rows, groups, name, what):
+    if t is None:
+        raise ValueError("out has no %s" % what)
+    if (t.dtype is not torch.uint8 or t.numel() < blocked_scale_bytes(rows, groups) or not t.is_cuda
+            or not t.is_contiguous()):
+        _check_bytes(t, blocked_scale_bytes(rows, groups), name)
+    return t.data_ptr()
+
+
 def _result(out, rows, cols, flag, dev):
-    """`out`, checked, or new memory for a [rows, cols] result in the layout."""
+    """`out`, checked, or new memory for a [rows, cols] result in the layout, and the C call's q, ld_q, s, qt, ld_qt,
+    st, bf16, ld_bf16 for it."""
     if flag == _lib.PURO_BF16:
         if out is None:
-            return torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-        if not isinstance(out, torch.Tensor):
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        elif not isinstance(out, torch.Tensor):
             raise ValueError("out must be a BF16 tensor for layout 'bf16'")
-        _check_tensor(out, (rows, cols), (torch.bfloat16,), "out")
-        return out
+        return out, (None, 0, None, None, 0, None, *_bf16(out, (rows, cols), "out"))
+    tiles = (rows + 127) // 128
     if out is None:
         out = QuantAct(rows, cols)
         if flag & _lib.PURO_ROWWISE:
@@ -70,44 +100,36 @@ def _result(out, rows, cols, flag, dev):
             out.s = _blocked(rows, cols // 128, dev)
         if flag & _lib.PURO_COLWISE:
             out.qt = torch.empty((cols, _round16(rows)), dtype=torch.uint8, device=dev)
-            out.st = _blocked(cols, (rows + 127) // 128, dev)
-        return out
-    if not isinstance(out, QuantAct) or (out.rows, out.cols) != (rows, cols):
+            out.st = _blocked(cols, tiles, dev)
+    elif not isinstance(out, QuantAct) or (out.rows, out.cols) != (rows, cols):
         raise ValueError("out must be a QuantAct made for a [%d, %d] input" % (rows, cols))
+    q = ld_q = s = qt = ld_qt = st = None
     if flag & _lib.PURO_ROWWISE:
-        _check_tensor(_need(out.q, "out has no row-wise codes"), (rows, cols), (torch.uint8,), "out.q")
-        _check_bytes(_need(out.s, "out has no row-wise scales"), blocked_scale_bytes(rows, cols // 128), "out.s")
+        q, ld_q = _codes(out.q, rows, cols, "out.q", "row-wise codes")
+        s = _scales(out.s, rows, cols // 128, "out.s", "row-wise scales")
     if flag & _lib.PURO_COLWISE:
-        _check_tensor(_need(out.qt, "out has no transposed codes"), (cols, _round16(rows)), (torch.uint8,), "out.qt",
-                      min_cols=True)
-        _check_bytes(_need(out.st, "out has no transposed scales"), blocked_scale_bytes(cols, (rows + 127) // 128),
-                     "out.st")
-    return out
+        qt, ld_qt = _codes(out.qt, cols, _round16(rows), "out.qt", "transposed codes", padded=True)
+        st = _scales(out.st, cols, tiles, "out.st", "transposed scales")
+    return out, (q, ld_q or 0, s, qt, ld_qt or 0, st, None, 0)
 
 
-def _result_args(res, flag):
-    """q, ld_q, s, qt, ld_qt, st, bf16, ld_bf16 of the C call."""
-    if res is None:
-        return (None, 0, None, None, 0, None, None, 0)
-    if flag == _lib.PURO_BF16:
-        return (None, 0, None, None, 0, None, res.data_ptr(), res.stride(0))
-    row, col = flag & _lib.PURO_ROWWISE, flag & _lib.PURO_COLWISE
-    return (_ptr(res.q) if row else None, _ld(res.q) if row else 0, _ptr(res.s) if row else None,
-            _ptr(res.qt) if col else None, _ld(res.qt) if col else 0, _ptr(res.st) if col else None, None, 0)
+_NO_RESULT = (None, 0, None, None, 0, None, None, 0)
 
 
 def _weight(w, cols, name):
+    if (w.dtype is torch.bfloat16 or w.dtype is torch.float32) and w.shape == (cols,) and w.is_cuda and w.is_contiguous():
+        return w.data_ptr()
     if not w.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if w.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("%s must be torch.bfloat16 or torch.float32, got %s" % (name, w.dtype))
-    if tuple(w.shape) != (cols,) or not w.is_contiguous():
-        raise ValueError("%s must be a contiguous [%d] tensor, got %s" % (name, cols, tuple(w.shape)))
+    raise ValueError("%s must be a contiguous [%d] tensor, got %s" % (name, cols, tuple(w.shape)))
 
 
 def _vector(t, n, name):
-    if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA float32 [%d] tensor" % (name, n))
+    return t.data_ptr()
 
 
 def _gate(gate, rows, cols):
@@ -142,6 +164,11 @@ def _same_type(w_pre, w_post):
     return int(w_pre.dtype == torch.float32)
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows, cols, flag, backward):
+    return _lib.puro_fp8_residual_norm_workspace_bytes(rows, cols, flag, backward)
+
+
 def _branch(h, w_post, gate):
     if h is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate act on the block output h, which is missing")
@@ -158,34 +185,37 @@ def residual_norm(x: torch.Tensor, w_pre: torch.Tensor, h: torch.Tensor | None =
     norm is taken.  gate is [rows, 1], [1, cols] or [rows, cols].  The stored (BF16) y is what the norm sees.
     `y` may be x itself (the sum is then taken in place)."""
     _require(x, torch.bfloat16, "x")
-    rows, cols = x.shape
+    shape = x.shape
+    rows, cols = shape
     flag = _layout_flag(layout)
     _branch(h, w_post, gate)
     if not eps > 0:
         raise ValueError("eps must be positive")
-    _weight(w_pre, cols, "w_pre")
+    w_pre_p = _weight(w_pre, cols, "w_pre")
     w_f32 = _same_type(w_pre, w_post)
     dev = x.device
+    h_p = y_p = w_post_p = None
+    ld_h = ld_y = 0
     if h is not None:
-        _check_tensor(h, (rows, cols), (torch.bfloat16,), "h")
+        h_p, ld_h = _bf16(h, shape, "h")
         if y is None:
-            y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-        _check_tensor(y, (rows, cols), (torch.bfloat16,), "y")
+            y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        y_p, ld_y = _bf16(y, shape, "y")
         if w_post is not None:
-            _weight(w_post, cols, "w_post")
+            w_post_p = _weight(w_post, cols, "w_post")
     elif y is not None:
         raise ValueError("y is only written with a block output h")
     kind, g_f32, ld_gate = _gate(gate, rows, cols)
-    res = _result(out, rows, cols, flag, dev)
-    # one allocation: the workspace (64 words) and the factors
-    buf = torch.empty(64 + (rows if w_post is None else 2 * rows), dtype=torch.float32, device=dev)
-    rstd = buf[64:64 + rows]
-    rstd_post = buf[64 + rows:] if w_post is not None else None
+    res, res_args = _result(out, rows, cols, flag, dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd_post = torch.empty(rows, dtype=torch.float32, device=dev) if w_post is not None else None
+    need = _norm_workspace(rows, cols, flag, 0)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = _lib.puro_fp8_residual_norm(
-        x.data_ptr(), x.stride(0), _ptr(h), _ld(h), w_pre.data_ptr(), _ptr(w_post), w_f32, _ptr(gate), ld_gate, kind,
-        g_f32, scale, eps, rows, cols, _ptr(y), _ld(y), rstd.data_ptr(), _ptr(rstd_post), flag,
-        *_result_args(res, flag), buf.data_ptr(), _stream())
-    _check(st, "puro_fp8_residual_norm")
+        x.data_ptr(), x.stride(0), h_p, ld_h, w_pre_p, w_post_p, w_f32, _ptr(gate), ld_gate, kind, g_f32, scale, eps,
+        rows, cols, y_p, ld_y, rstd.data_ptr(), _ptr(rstd_post), flag, *res_args, _ptr(ws), _stream())
+    if st:
+        _check(st, "puro_fp8_residual_norm")
     return ResidualNorm(x if h is None else y, res, rstd, rstd_post)
 
 
@@ -204,25 +234,28 @@ def residual_norm_backward(dn: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor
     accumulate=True the weights' gradients, and the gradient of a gate [1, cols], are added into the given FP32
     buffers."""
     _require(dn, torch.bfloat16, "dn")
-    rows, cols = dn.shape
+    shape = dn.shape
+    rows, cols = shape
     flag = _layout_flag(layout)
     _branch(h, w_post, gate)
-    _check_tensor(y, (rows, cols), (torch.bfloat16,), "y")
-    _vector(rstd, rows, "rstd")
-    _weight(w_pre, cols, "w_pre")
+    y_p, ld_y = _bf16(y, shape, "y")
+    rstd_p = _vector(rstd, rows, "rstd")
+    w_pre_p = _weight(w_pre, cols, "w_pre")
     w_f32 = _same_type(w_pre, w_post)
     dev = dn.device
+    dy_p = h_p = w_post_p = rstd_post_p = dw_post_p = None
+    ld_dy = ld_h = 0
     if dy is not None:
-        _check_tensor(dy, (rows, cols), (torch.bfloat16,), "dy")
+        dy_p, ld_dy = _bf16(dy, shape, "dy")
     if h is not None:
-        _check_tensor(h, (rows, cols), (torch.bfloat16,), "h")
+        h_p, ld_h = _bf16(h, shape, "h")
     if w_post is not None:
-        _weight(w_post, cols, "w_post")
-        _vector(_need(rstd_post, "w_post needs the rstd_post of the forward pass"), rows, "rstd_post")
+        w_post_p = _weight(w_post, cols, "w_post")
+        rstd_post_p = _vector(_need(rstd_post, "w_post needs the rstd_post of the forward pass"), rows, "rstd_post")
     kind, g_f32, ld_gate = _gate(gate, rows, cols)
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    _check_tensor(dx, (rows, cols), (torch.bfloat16,), "dx")
+        dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    dx_p, ld_dx = _bf16(dx, shape, "dx")
     if h is None and out is not None:
         raise ValueError("out holds the gradient of h, which is missing")
     if (w_post is None and dw_post is not None) or (gate is None and dgate is not None):
@@ -232,27 +265,26 @@ def residual_norm_backward(dn: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor
         raise ValueError("accumulate=True needs the FP32 buffers to add into")
     if dw_pre is None:
         dw_pre = torch.empty(cols, dtype=torch.float32, device=dev)
-    _vector(dw_pre, cols, "dw_pre")
+    dw_pre_p = _vector(dw_pre, cols, "dw_pre")
     if w_post is not None:
         if dw_post is None:
             dw_post = torch.empty(cols, dtype=torch.float32, device=dev)
-        _vector(dw_post, cols, "dw_post")
+        dw_post_p = _vector(dw_post, cols, "dw_post")
     if gate is not None:
         gtype = torch.bfloat16 if kind == _lib.PURO_GATE_FULL else torch.float32
         if dgate is None:
-            dgate = torch.empty(tuple(gate.shape), dtype=gtype, device=dev)
-        _check_tensor(dgate, tuple(gate.shape), (gtype,), "dgate")
+            dgate = torch.empty(gate.shape, dtype=gtype, device=dev)
+        _check_tensor(dgate, gate.shape, (gtype,), "dgate")
         if kind == _lib.PURO_GATE_TOKEN and not dgate.is_contiguous():
             raise ValueError("dgate must be contiguous")
-    res = _result(out, rows, cols, flag, dev) if h is not None else None
-    ws = torch.empty(max(_lib.puro_fp8_residual_norm_workspace_bytes(rows, cols, flag if h is not None else 0, 1), 16),
-                     dtype=torch.uint8, device=dev)
+    res, res_args = _result(out, rows, cols, flag, dev) if h is not None else (None, _NO_RESULT)
+    ws = torch.empty(_norm_workspace(rows, cols, flag if h is not None else 0, 1), dtype=torch.uint8, device=dev)
     st = _lib.puro_fp8_residual_norm_backward(
-        dn.data_ptr(), dn.stride(0), _ptr(dy), _ld(dy), y.data_ptr(), y.stride(0), rstd.data_ptr(), _ptr(h), _ld(h),
-        _ptr(rstd_post), w_pre.data_ptr(), _ptr(w_post), w_f32, _ptr(gate), ld_gate, kind, g_f32, scale, rows, cols,
-        dx.data_ptr(), dx.stride(0), dw_pre.data_ptr(), _ptr(dw_post), _ptr(dgate), _ld(dgate),
-        1 if accumulate else 0, flag, *_result_args(res, flag), ws.data_ptr(), _stream())
-    _check(st, "puro_fp8_residual_norm_backward")
+        dn.data_ptr(), dn.stride(0), dy_p, ld_dy, y_p, ld_y, rstd_p, h_p, ld_h, rstd_post_p, w_pre_p, w_post_p, w_f32,
+        _ptr(gate), ld_gate, kind, g_f32, scale, rows, cols, dx_p, ld_dx, dw_pre_p, dw_post_p, _ptr(dgate), _ld(dgate),
+        1 if accumulate else 0, flag, *res_args, ws.data_ptr(), _stream())
+    if st:
+        _check(st, "puro_fp8_residual_norm_backward")
     return ResidualNormGrad(dx, dw_pre, res, dw_post, dgate)
 
 
@@ -265,9 +297,10 @@ def swiglu(gu: torch.Tensor, layout: str = "both", out: QuantAct | torch.Tensor 
     flag = _layout_flag(layout)
     if f2 % 2:
         raise ValueError("gu must hold two halves of equal width, got %d columns" % f2)
-    res = _result(out, rows, f2 // 2, flag, gu.device)
-    st = _lib.puro_fp8_swiglu(gu.data_ptr(), gu.stride(0), rows, f2 // 2, flag, *_result_args(res, flag), _stream())
-    _check(st, "puro_fp8_swiglu")
+    res, res_args = _result(out, rows, f2 // 2, flag, gu.device)
+    st = _lib.puro_fp8_swiglu(gu.data_ptr(), gu.stride(0), rows, f2 // 2, flag, *res_args, _stream())
+    if st:
+        _check(st, "puro_fp8_swiglu")
     return res
 
 
@@ -279,9 +312,9 @@ def swiglu_backward(da: torch.Tensor, gu: torch.Tensor, layout: str = "both",
     _require(da, torch.bfloat16, "da")
     rows, f = da.shape
     flag = _layout_flag(layout)
-    _check_tensor(gu, (rows, 2 * f), (torch.bfloat16,), "gu")
-    res = _result(out, rows, 2 * f, flag, gu.device)
-    st = _lib.puro_fp8_swiglu_backward(da.data_ptr(), da.stride(0), gu.data_ptr(), gu.stride(0), rows, f, flag,
-                                       *_result_args(res, flag), _stream())
-    _check(st, "puro_fp8_swiglu_backward")
+    gu_p, ld_gu = _bf16(gu, (rows, 2 * f), "gu")
+    res, res_args = _result(out, rows, 2 * f, flag, gu.device)
+    st = _lib.puro_fp8_swiglu_backward(da.data_ptr(), da.stride(0), gu_p, ld_gu, rows, f, flag, *res_args, _stream())
+    if st:
+        _check(st, "puro_fp8_swiglu_backward")
     return res

@@ -195,6 +195,12 @@ int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, co
   return launch_status();
 }
 
+// A B200's SMs (fixed, so that what depends on them does not depend on the
+// device's state).
+constexpr int64_t kSms = 148;
+
+bool quant_short_stream(int64_t tiles) { return tiles <= 8 * 2 * kSms; }
+
 // Short tile streams (up to about 8 tiles per CTA at two CTAs per SM): two
 // stages, two CTAs per SM, a static tile schedule.  Longer streams: one
 // stage, three CTAs per SM, and the tiles after each CTA's first handed out
@@ -209,7 +215,7 @@ int launch_quant_cfg(const void* x, int64_t ld_x, const puro::QuantParams& p, co
 template <bool ROW, bool COL, bool BLOCK, bool NORM = false>
 int launch_quant(const void* x, int64_t ld_x, const puro::QuantParams& p, const DeviceInfo& dev,
                  cudaStream_t stream) {
-  const bool short_stream = p.tiles <= 8 * 2 * (int64_t)dev.sms;
+  const bool short_stream = quant_short_stream(p.tiles);
   puro::QuantParams ps = p;
   if (BLOCK || short_stream) ps.ctr = nullptr;
   // the kernel's division-free tile decode (tiles_c >= 1 here; < 2^24)
@@ -898,13 +904,12 @@ puro::QuantParams quant_params(const puro::CodeOut& o, int64_t rows, int64_t col
 }
 
 // Rows that a CTA of a row pass takes: 32, or fewer, down to `least`, where that
-// would leave an SM without its `resident` CTAs.  (148 SMs: the split, and with
-// it the order in which the backward pass adds its sums over tokens, does not
-// depend on the device's state.)
-constexpr int64_t kNormSms = 148;
+// would leave an SM without its `resident` CTAs.  (The split, and with it the
+// order in which the backward pass adds its sums over tokens, depends on the
+// sizes alone.)
 int norm_rpc(int64_t rows, int64_t resident, int least) {
   int rpc = 32;
-  while (rpc > least && rows < rpc * resident * kNormSms) rpc /= 2;
+  while (rpc > least && rows < rpc * resident * kSms) rpc /= 2;
   return rpc;
 }
 int norm_backward_rpc(int64_t rows, int64_t cols) {
@@ -1052,9 +1057,11 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
   const bool col = p.out.qt != nullptr;
   const puro::CodeOut out = p.out;
   if (col) {
-    if (!workspace) return PURO_ERR_NULL;
-    if (!aligned16(workspace)) return PURO_ERR_ALIGN;
-    p.ctr = static_cast<uint32_t*>(workspace);
+    if (puro_fp8_residual_norm_workspace_bytes(rows, cols, layout, 0)) {
+      if (!workspace) return PURO_ERR_NULL;
+      if (!aligned16(workspace)) return PURO_ERR_ALIGN;
+      p.ctr = static_cast<uint32_t*>(workspace);
+    }
     p.out = puro::CodeOut{};
   }
   DeviceInfo* dev = nullptr;
@@ -1087,7 +1094,7 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
 int64_t puro_fp8_residual_norm_workspace_bytes(int64_t rows, int64_t cols, int layout, int backward) {
   if (rows <= 0 || cols <= 0) return 0;
   const bool col = layout == PURO_COLWISE || layout == PURO_BOTH;
-  if (!backward) return col ? kNormCounterBytes : 0;
+  if (!backward) return col && !quant_short_stream((rows + 127) / 128 * (cols / 128)) ? kNormCounterBytes : 0;
   return kNormCounterBytes + norm_part_bytes(rows, cols) + (col ? rows * cols * 2 : 0);
 }
 

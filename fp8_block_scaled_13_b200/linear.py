@@ -35,16 +35,18 @@ def _blocked(rows: int, groups: int, dev) -> torch.Tensor:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream() -> int:
     """The current CUDA stream of the current device, as a cudaStream_t value."""
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
 _FIELD_NAMES: dict = {}
+_PLAIN = frozenset((str, bool, int, float))
 
 
 def _tensors(obj):
@@ -53,9 +55,10 @@ def _tensors(obj):
         return (obj,)
     names = _FIELD_NAMES.get(type(obj))
     if names is None:
-        if not dataclasses.is_dataclass(obj) or isinstance(obj, type):
-            return ()
-        names = _FIELD_NAMES[type(obj)] = tuple(f.name for f in dataclasses.fields(obj))
+        names = ()
+        if dataclasses.is_dataclass(obj) and not isinstance(obj, type):
+            names = tuple(f.name for f in dataclasses.fields(obj))
+        _FIELD_NAMES[type(obj)] = names
     return tuple(v for v in (getattr(obj, n) for n in names) if isinstance(v, torch.Tensor))
 
 
@@ -69,14 +72,16 @@ def _on_operand_device(fn):
         operands = (*args, *kwargs.values()) if kwargs else args
         dev = None
         for a in operands:
-            for t in _tensors(a):
+            if a is None or type(a) in _PLAIN:
+                continue
+            for t in (a,) if type(a) is torch.Tensor else _tensors(a):
                 if dev is None:
                     dev = t.device
                 elif t.device != dev:
                     devs = {t.device for a in operands for t in _tensors(a)}
                     raise ValueError("%s: operands are on different devices (%s)"
                                      % (fn.__name__, ", ".join(sorted(str(d) for d in devs))))
-        if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        if dev is not None and dev.type == "cuda" and dev.index != _current_device():
             with torch.cuda.device(dev):
                 return fn(*args, **kwargs)
         return fn(*args, **kwargs)

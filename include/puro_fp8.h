@@ -323,7 +323,8 @@ PURO_API int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, 
                                     void* n, int64_t ld_n, void* workspace, void* stream);
 
 /* Bytes of the workspace (16-byte aligned, contents don't matter) of
- * puro_fp8_residual_norm (backward = 0: 0 or 256 bytes) and of
+ * puro_fp8_residual_norm (backward = 0: 256 where many transposed codes are
+ * made, else 0) and of
  * puro_fp8_residual_norm_backward (backward = 1), for outputs in `layout`
  * (0: backward without h).  Calls that may run at the same time need distinct
  * ones. */

@@ -99,7 +99,6 @@ def _norm(**over):
     (dict(x=None), -1), (dict(w_pre=None), -1), (dict(y=None), -1), (dict(rstd=None), -1), (dict(rstd_post=None), -1),
     (dict(gate=None), -1), (dict(q=None), -1), (dict(s=None), -1), (dict(qt=None), -1), (dict(st=None), -1),
     (dict(layout=4), -1),                                        # BF16 result without its buffer
-    (dict(workspace=None), -1), (dict(layout=2, workspace=None), -1), (dict(workspace=A + 8), -2),
     (dict(ld_x=128), -3), (dict(ld_h=128), -3), (dict(ld_y=128), -3), (dict(ld_gate=128), -3),
     (dict(ld_qt=48), -3), (dict(layout=4, n=A, ld_n=128), -3),
     (dict(x=A + 2), -2), (dict(h=A + 8), -2), (dict(ld_x=260), -2), (dict(w_pre=A + 1), -2), (dict(rstd=A + 2), -2),
@@ -107,6 +106,13 @@ def _norm(**over):
 ])
 def test_norm_argument_errors(lib, over, code):
     assert lib.puro_fp8_residual_norm(*_norm(**over), None) == code
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(workspace=None), -1), (dict(layout=2, workspace=None), -1), (dict(workspace=A + 8), -2)])
+def test_norm_wants_its_workspace(lib, over, code):
+    big = dict(rows=1 << 18, ld_qt=1 << 18)
+    assert lib.puro_fp8_residual_norm(*_norm(**big, **over), None) == code
 
 
 def _norm_bwd(**over):
@@ -164,7 +170,9 @@ def test_workspace_sizes(lib):
     size = lib.puro_fp8_residual_norm_workspace_bytes
     for layout in (0, 1, 2, 3, 4):
         assert size(0, 256, layout, 0) == size(0, 256, layout, 1) == size(5, 0, layout, 1) == 0
-    assert [size(129, 256, layout, 0) for layout in (1, 2, 3, 4)] == [0, 256, 256, 0]
+    # forward: a tile counter where transposed codes take more than 2368 tiles
+    assert [size(32768, 2048, layout, 0) for layout in (1, 2, 3, 4)] == [0, 256, 256, 0]
+    assert size(148 * 128, 2048, 3, 0) == 0 and size(148 * 128 + 1, 2048, 3, 0) == 256
     for rows in (1, 4, 5, 129, 1000, 9471, 9472, 32768, 1 << 24):
         for cols in (128, 2048, 4096, 8192):
             sums = size(rows, cols, 1, 1)
