@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import dataclasses
 import functools
+import operator
 from dataclasses import dataclass
 
 import torch
@@ -45,21 +46,26 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-_FIELD_NAMES: dict = {}
-_PLAIN = frozenset((str, bool, int, float))
+_FIELDS: dict = {}
+_PLAIN = frozenset((str, bool, int, float, type(None)))
 
 
 def _tensors(obj):
     """The tensors of a wrapper argument: a tensor, or a dataclass's tensor fields."""
     if isinstance(obj, torch.Tensor):
         return (obj,)
-    names = _FIELD_NAMES.get(type(obj))
-    if names is None:
-        names = ()
+    get = _FIELDS.get(type(obj))
+    if get is None:
+        get = _no_fields
         if dataclasses.is_dataclass(obj) and not isinstance(obj, type):
-            names = tuple(f.name for f in dataclasses.fields(obj))
-        _FIELD_NAMES[type(obj)] = names
-    return tuple(v for v in (getattr(obj, n) for n in names) if isinstance(v, torch.Tensor))
+            names = [f.name for f in dataclasses.fields(obj)]
+            get = operator.attrgetter(*names, "__class__")  # (a tuple even of one field)
+        _FIELDS[type(obj)] = get
+    return [v for v in get(obj) if type(v) not in _PLAIN and isinstance(v, torch.Tensor)]
+
+
+def _no_fields(obj):
+    return ()
 
 
 def _on_operand_device(fn):
@@ -72,9 +78,10 @@ def _on_operand_device(fn):
         operands = (*args, *kwargs.values()) if kwargs else args
         dev = None
         for a in operands:
-            if a is None or type(a) in _PLAIN:
+            kind = type(a)
+            if kind in _PLAIN:
                 continue
-            for t in (a,) if type(a) is torch.Tensor else _tensors(a):
+            for t in (a,) if kind is torch.Tensor else _tensors(a):
                 if dev is None:
                     dev = t.device
                 elif t.device != dev:
