@@ -26,14 +26,29 @@
 // times 2^12, which holds while |X| < 64, |M| < 8 and |R| < 16 off the
 // diagonal; the iteration keeps singular values near 1.
 //
-// All three products of a step are one kernel, D[i, j] = sum_k P[i, k] Q[j, k]:
-// tcgen05 kind::f16 on CTA pairs (256-row tiles), FP32 accumulators in TMEM,
-// fed by TMA.  An operand that is stored the other way round ([k][i]) is read
-// MN-major, so nothing is ever transposed in memory.  M and R are symmetric:
-// only tiles on or below the diagonal are computed and the epilogue writes
-// each one also to its mirrored place; with 256 x 128 tiles a 2048-wide M is 72
-// units, one wave of the 74 CTA pairs.  Bound by the tensor cores for large G, by launches
-// (2 + 3 steps, overlapped by programmatic dependent launch) for small ones.
+// A whole call is one cooperative launch after two passes over G (its norm, and
+// the two FP16 terms of X0).  Its 3 * steps products D[i, j] = sum_k A[i, k]
+// B[j, k] follow each other over a barrier of the grid's CTAs: the next
+// product's loads wait for it, everything else (TMEM, barriers, tensor maps)
+// stays set up.  (One launch per product cost 3.8 us each in tails and starts:
+// @)
+//
+// A product runs tcgen05 kind::f16 on CTA pairs, 256 x 256 tiles, FP32
+// accumulators in TMEM (two, so that a tile's epilogue overlaps the next one's
+// products), fed by TMA through a ring of 64-deep stages.  256 columns let the
+// loads (64 bytes a clock and SM at the full rate) just follow the tensor
+// cores; 128 columns need 96 and got 0.57 of the rate.  An operand that is
+// stored the other way round ([k][i]) is read MN-major, so nothing is ever
+// transposed in memory.  M and R are symmetric: only tiles on or below the
+// diagonal are computed, and the epilogue writes each one also to its mirrored
+// place.  The tiles that do not fill a round of all CTA pairs are split along
+// k over the idle pairs; each of them leaves the FP32 partials that it does not
+// own in the workspace, waits for the others' and finishes its own share of the
+// columns, so the epilogue is split as well.  (2048 x 2048: 36 tiles of M
+// become 72 half tiles on 74 pairs.)
+// The epilogue's own inputs (O, or both terms of X) come by TMA into the buffer
+// that the result then leaves from, a chunk of 32 x 32 ahead.  Bound by the
+// tensor cores for large G, by the 3 * steps hand-overs for small ones.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,54 +58,69 @@
 
 namespace puro {
 
-enum OrthoEpilogue : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2 };
+enum OrthoProduct : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2 };
 
 constexpr int kOrthoNormBlocks = 592;  // CTAs of the norm pass, one partial sum each
 constexpr int64_t kOrthoExactK = 1024; // longest X X^T sum that takes three products
 constexpr float kXScale = 1024.f, kMScale = 8192.f, kRScale = 4096.f;
+constexpr int kOrthoMaxSplit = 8;
 
-struct OrthoParams {
+// One of the three products, as every step takes it.  Unit u < full is a whole
+// tile; the units after them are the remaining tiles in `split` parts each.
+struct OrthoShape {
   int32_t rows_a, rows_b;   // D is [rows_a, rows_b]
   int32_t kblocks;          // ceil(K / 64)
   int32_t passes;           // 1: hi hi; 3: hi hi, hi lo, lo hi
-  int32_t tiles_m, tiles_n;
-  int32_t units;            // tiles; kOrthoGram / kOrthoPoly: those on or below the diagonal
-  float a, b, c;
-  float* diag;              // Gram: D written; Poly: D read
-  float* diag_r;            // Poly: D' written; Update: D' read
-  const __half* src_hi;     // Poly: O (times 2^13); Update: X hi
-  const __half* src_lo;     // Update: X lo
-  int64_t ld_src;
-  __nv_bfloat16* out;       // last step: the BF16 result
-  int64_t ld_out;
-  int32_t col_diag;         // Update: D' goes by column (tall G)
-  int32_t last, out_tma;    // last step; the result goes out by TMA (else by plain stores)
+  int32_t tiles_m;          // kOrthoUpdate: tiles down (the others count the lower triangle)
+  int32_t full, split, units;
 };
 
-template <int BN>
+struct OrthoParams {
+  OrthoShape shape[3];
+  int32_t steps;
+  float a, b, c;
+  float* diag;              // D, the diagonal of M
+  float* diag_r;            // D', the diagonal of R
+  uint32_t* grid_count;     // arrivals at the grid barrier; zero before the launch
+  uint32_t* tile_count;     // [3][kSplitTiles][2] arrivals of a split tile's parts; zero before the launch
+  float4* partial;          // [units of split tiles][2][8][4][8][32]
+  __nv_bfloat16* out;       // the BF16 result, by plain stores if out_tma is 0
+  int64_t ld_out;
+  int32_t out_tma;
+};
+constexpr int kSplitTiles = 74;  // most tiles that can be split: fewer than CTA pairs
+constexpr int kOrthoCounters = 64 + 3 * kSplitTiles * 2;
+
+// Tensor maps.  Operands: 64-wide boxes with the 128-byte swizzle, 128 rows
+// (K-major) or 64 (MN-major); epilogue: boxes of 32 x 32 with the 64-byte one.
+struct OrthoMaps {
+  CUtensorMap gram[2][2];   // X as the operands of X X^T: [buffer][hi, lo]
+  CUtensorMap update[2];    // X hi as an operand of the update
+  CUtensorMap o, r;         // O (both operands of the square), R (an operand of the update)
+  CUtensorMap ex[2][2], eo, er, out;
+};
+
 struct OrthoCfg {
-  static constexpr int kBM = 256;              // tile rows (a CTA pair)
-  static constexpr int kBNC = BN / 2;          // rows of Q in each CTA
-  static constexpr uint32_t kTileA = 128 * 128;       // 128 rows x 64 FP16
-  static constexpr uint32_t kTileB = kBNC * 128;
-  static constexpr uint32_t kStageBytes = kTileA + kTileB;
-  static constexpr int kStages = BN == 256 ? 6 : 8;   // 192 KB
+  static constexpr uint32_t kTile = 128 * 128;        // 128 rows x 64 FP16
+  static constexpr uint32_t kStageBytes = 2 * kTile;  // A and B of one CTA
+  static constexpr int kStages = 4;                   // 128 KB
   static constexpr int kEpiWarps = 8;
-  static constexpr int kEpiCols = BN / 2;
-  static constexpr uint32_t kEpiBytes = kEpiWarps * 4096;  // hi and lo, 32 rows x 64 bytes each
+  static constexpr uint32_t kBuf = 4096;              // hi and lo (or mirrored), 32 rows x 64 bytes each
+  static constexpr int kBufs = 3;                     // a warp's chunks in flight
+  static constexpr uint32_t kEpiBytes = kEpiWarps * kBufs * kBuf;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kOffEpi = kStages * kStageBytes;
   static constexpr uint32_t kOffBar = kOffEpi + kEpiBytes;
-  static constexpr uint32_t kNumBars = 2 * kStages + 5;
+  static constexpr uint32_t kNumBars = 2 * kStages + 5 + 4 + kBufs * kEpiWarps;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-  static constexpr uint32_t kTmemCols = 2 * BN;       // two accumulators
+  static constexpr uint32_t kTmemCols = 512;          // two accumulators
 };
 
 // D[tmem] (+)= A B^T for one M = 256, K = 16 slice of FP16 operands of the CTA pair.
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+                                           uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -108,23 +138,43 @@ __device__ __forceinline__ uint64_t desc_sw128_mnmajor(uint32_t saddr) {
          (1ull << 46) | (2ull << 61);
 }
 
-// Tile (tm, tn) of unit u.  Symmetric results count the 128-column tiles on or
-// below the diagonal row block by row block (2 I + 2 of them in row block I).
+struct OrthoUnit {
+  int32_t tm, tn;       // 256 x 256 tile
+  int32_t cols;         // columns of D that it computes: a multiple of 32, 256 at most
+  int32_t k0, k1;       // its 64-deep blocks, of kblocks * passes
+  int32_t part, parts;  // its place among the parts of a split tile
+  int32_t index;        // of the split tile
+};
+
 template <bool SYM>
-__device__ __forceinline__ void ortho_tile(const OrthoParams& p, int u, int& tm, int& tn) {
-  if (SYM) {
-    int i = 0;
-    for (;; ++i) {
-      const int n = 2 * i + 2 < p.tiles_n ? 2 * i + 2 : p.tiles_n;
-      if (u < n) break;
-      u -= n;
-    }
-    tm = i;
-    tn = u;
-  } else {
-    tn = u / p.tiles_m;
-    tm = u - tn * p.tiles_m;
+__device__ __forceinline__ OrthoUnit ortho_unit(const OrthoShape& s, int32_t u) {
+  OrthoUnit r;
+  const int32_t total = s.kblocks * s.passes;
+  int32_t t = u;
+  r.part = 0;
+  r.parts = 1;
+  r.index = 0;
+  if (u >= s.full) {
+    r.index = (u - s.full) / s.split;
+    r.part = u - s.full - r.index * s.split;
+    r.parts = s.split;
+    t = s.full + r.index;
   }
+  r.k0 = (int32_t)((int64_t)total * r.part / r.parts);
+  r.k1 = (int32_t)((int64_t)total * (r.part + 1) / r.parts);
+  if (SYM) {
+    // row by row of the lower triangle
+    int32_t i = 0;
+    for (; t > i; ++i) t -= i + 1;
+    r.tm = i;
+    r.tn = t;
+  } else {
+    r.tn = t / s.tiles_m;
+    r.tm = t - r.tn * s.tiles_m;
+  }
+  const int32_t left = s.rows_b - r.tn * 256;
+  r.cols = left >= 256 ? 256 : (left + 31) / 32 * 32;
+  return r;
 }
 
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
@@ -136,51 +186,421 @@ __device__ __forceinline__ float2 half_unpack(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
-template <int BN, bool AMN, bool BMN, int EPI>
-__global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
-    ortho_gemm_kernel(const __grid_constant__ CUtensorMap tm_ah, const __grid_constant__ CUtensorMap tm_al,
-                      const __grid_constant__ CUtensorMap tm_bh, const __grid_constant__ CUtensorMap tm_bl,
-                      const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ CUtensorMap tm_dl,
-                      const __grid_constant__ OrthoParams p) {
-  using C = OrthoCfg<BN>;
-  constexpr int S = C::kStages;
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void count_arrive(uint32_t* c) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c) : "memory");
+}
+
+// Waits, bounded as every wait here, until *c has reached `target`.  (The
+// release of an arrival covers what the arriving thread has learned of other
+// threads' writes through a shared-memory barrier.)
+__device__ __forceinline__ bool count_wait(const uint32_t* c, uint32_t target, volatile int* abort) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+    if ((int32_t)(v - target) >= 0) return true;
+    if ((it & 15u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        record_error(kErrDeviceTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+struct OrthoSmem {
+  uint8_t* base;
+  uint64_t *full, *empty, *accf, *acce, *drain, *ready, *done, *parts_out, *parts_in, *src;
+  volatile int* abort_flag;
+};
+
+// The producer warp's share of one product.
+template <bool SYM, bool AMN, bool BMN>
+__device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape& s, const CUtensorMap* ah,
+                                           const CUtensorMap* al, const CUtensorMap* bh, const CUtensorMap* bl,
+                                           int cluster_id, int clusters, uint32_t rank, int& stage, uint32_t& phase,
+                                           uint32_t& issued, uint32_t& issued_phase) {
+  using C = OrthoCfg;
+  for (int32_t u = cluster_id; u < s.units; u += clusters) {
+    const OrthoUnit t = ortho_unit<SYM>(s, u);
+    const int32_t a0 = t.tm * 256 + 128 * (int32_t)rank;
+    const int32_t b0 = t.tn * 256 + (t.cols >> 1) * (int32_t)rank;
+    for (int32_t i = t.k0; i < t.k1; ++i) {
+      const int32_t pass = s.passes == 1 ? 0 : i / s.kblocks, k = (i - pass * s.kblocks) * 64;
+      if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1, sm.abort_flag)) return false;
+      if (elect_one()) {
+        if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], 2 * C::kStageBytes);
+        const uint32_t bar = leader_addr<2>(&sm.full[stage]);
+        uint8_t* da = sm.base + stage * C::kStageBytes;
+        uint8_t* db = da + C::kTile;
+        const CUtensorMap* ma = pass == 2 ? al : ah;
+        const CUtensorMap* mb = pass == 1 ? bl : bh;
+        if (AMN) {
+          tma_load_2d<2>(da, ma, a0, k, bar);
+          tma_load_2d<2>(da + 8192, ma, a0 + 64, k, bar);
+        } else {
+          tma_load_2d<2>(da, ma, k, a0, bar);
+        }
+        if (BMN) {
+          tma_load_2d<2>(db, mb, b0, k, bar);
+          tma_load_2d<2>(db + 8192, mb, b0 + 64, k, bar);
+        } else {
+          tma_load_2d<2>(db, mb, k, b0, bar);
+        }
+      }
+      issued |= 1u << stage;
+      issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  return true;
+}
+
+// The MMA warp's (leader CTA only).
+template <bool SYM, bool AMN, bool BMN>
+__device__ __forceinline__ bool ortho_mma(const OrthoSmem& sm, const OrthoShape& s, uint32_t tmem, int cluster_id,
+                                          int clusters, int& stage, uint32_t& phase, uint32_t& it) {
+  using C = OrthoCfg;
+  constexpr uint32_t kStepA = AMN ? 2048 >> 4 : 32 >> 4;  // 16 elements along k
+  constexpr uint32_t kStepB = BMN ? 2048 >> 4 : 32 >> 4;
+  const uint32_t base = smem_u32(sm.base);
+  const uint64_t a_desc0 = AMN ? desc_sw128_mnmajor(base) : desc_sw128_kmajor(base);
+  const uint64_t b_desc0 = BMN ? desc_sw128_mnmajor(base + C::kTile) : desc_sw128_kmajor(base + C::kTile);
+  for (int32_t u = cluster_id; u < s.units; u += clusters, ++it) {
+    const OrthoUnit t = ortho_unit<SYM>(s, u);
+    // D FP32, A and B FP16 (formats 0), MN-major flags, N, M
+    const uint32_t idesc = (1u << 4) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
+                           ((uint32_t)(t.cols >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+    const uint32_t acc = it & 1;
+    if (!mbar_wait_warp(&sm.acce[acc], ((it >> 1) & 1) ^ 1, sm.abort_flag)) return false;
+    tc_fence_after();
+    for (int32_t i = t.k0; i < t.k1; ++i) {
+      if (!mbar_wait_warp(&sm.full[stage], phase, sm.abort_flag)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t ad = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+        const uint64_t bd = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_f16(tmem + acc * 256, ad + k * kStepA, bd + k * kStepB, idesc, (i > t.k0 || k > 0) ? 1u : 0u);
+        tc_commit_all<2>(&sm.empty[stage]);
+      }
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) tc_commit_all<2>(&sm.accf[acc]);
+  }
+  return true;
+}
+
+// State of an epilogue warp that outlives a product.
+struct OrthoEpiState {
+  uint32_t it;         // tiles so far
+  uint32_t buf;        // the next chunk's buffer
+  uint32_t src_phase;  // phases of the source barriers
+  uint32_t splits;     // split tiles so far
+};
+
+// An epilogue warp's: 32 rows of D, every other chunk of 32 columns.  Buffers
+// hold rows of 64 bytes, their 16-byte pieces XORed with bits 1..2 of the row
+// (the 64-byte swizzle): lanes that each touch their own row meet no bank
+// twice.
+template <int EPI, bool TALL>
+__device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoParams& p, const CUtensorMap* src_hi,
+                                               const CUtensorMap* src_lo, const CUtensorMap* dst_hi,
+                                               const CUtensorMap* dst_lo, uint32_t tmem, int cluster_id, int clusters,
+                                               uint32_t rank, int step, OrthoEpiState& st) {
+  using C = OrthoCfg;
   constexpr bool SYM = EPI != kOrthoUpdate;
-  // D FP32, A and B FP16 (formats 0), MN-major flags, N, M
-  constexpr uint32_t kIdesc = (1u << 4) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
-                              ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(C::kBM >> 4) << 24);
+  constexpr bool kCols = EPI == kOrthoPoly || (EPI == kOrthoUpdate && TALL);  // a diagonal goes by column
+  const OrthoShape& s = p.shape[EPI];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sp = warp & 3, half = (warp - 2) >> 2;
+  const bool last = EPI == kOrthoUpdate && step == p.steps - 1;
+  uint8_t* bufs = sm.base + C::kOffEpi + (warp - 2) * C::kBufs * C::kBuf;
+  uint64_t* src_bar = sm.src + (warp - 2) * C::kBufs;
+  const int sw = (lane >> 1) & 3;  // this lane's row's swizzle
+  const float* diag = EPI == kOrthoPoly ? p.diag : p.diag_r;
+  for (int32_t u = cluster_id; u < s.units; u += clusters, ++st.it) {
+    const OrthoUnit t = ortho_unit<SYM>(s, u);
+    const uint32_t acc = st.it & 1;
+    const int32_t row0 = t.tm * 256 + 128 * (int32_t)rank + sp * 32, row = row0 + lane;
+    const int32_t chunks = t.cols >> 5;
+    const int32_t c0 = t.part + t.parts * half, dc = 2 * t.parts;  // this warp's chunks
+    const bool rows_in = row0 < s.rows_a;
+    const bool mirror = SYM && t.tn < t.tm;
+    // brings the epilogue's inputs of a chunk into a buffer
+    auto prefetch = [&](int32_t c, uint32_t b) {
+      uint8_t* buf = bufs + b * C::kBuf;
+      const int32_t x = t.tn * 256 + c * 32;
+      mbar_arrive_expect_tx(&src_bar[b], EPI == kOrthoUpdate ? 4096 : 2048);
+      tma_load_2d<1>(buf, src_hi, x, row0, smem_u32(&src_bar[b]));
+      if (EPI == kOrthoUpdate) tma_load_2d<1>(buf + 2048, src_lo, x, row0, smem_u32(&src_bar[b]));
+    };
+    auto after = [](uint32_t b, uint32_t n) { return b + n >= C::kBufs ? b + n - C::kBufs : b + n; };
+    if (EPI != kOrthoGram && rows_in && lane == 0) {
+      // every buffer's last store has read it by now, or is waited for
+      bulk_wait_group_read<0>();
+#pragma unroll
+      for (uint32_t n = 0; n < C::kBufs; ++n)
+        if (c0 + (int32_t)n * dc < chunks) prefetch(c0 + (int32_t)n * dc, after(st.buf, n));
+    }
+    float dr = 0.f;
+    if (row < s.rows_a && (EPI == kOrthoPoly || (EPI == kOrthoUpdate && !TALL))) dr = __ldcg(diag + row);
+    if (!mbar_wait_warp(&sm.accf[acc], (st.it >> 1) & 1, sm.abort_flag)) return false;
+    tc_fence_after();
+    const uint32_t t_base = tmem + ((uint32_t)(sp * 32) << 16) + acc * 256;
+    float4* part = p.partial + (int64_t)(u - s.full) * 2 * 8 * 4 * 8 * 32;
+    if (t.parts > 1) {
+      // the chunks that other parts own leave as FP32
+      for (int32_t c = half; c < chunks && rows_in; c += 2) {
+        if (c % t.parts == t.part) continue;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t_base + c * 32, r);
+        tmem_ld_wait();
+        regs_after_wait(r);
+        float4* d = part + (((int)rank * 8 + c) * 4 + sp) * 256 + lane;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          d[q * 32] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                  __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.parts_out);
+      if (warp == 2) {
+        if (!mbar_wait_warp(sm.parts_out, st.splits & 1, sm.abort_flag)) return false;
+        bool ok = true;
+        if (lane == 0) {
+          uint32_t* count = p.tile_count + (EPI * kSplitTiles + t.index) * 2 + rank;
+          count_arrive(count);
+          ok = count_wait(count, (uint32_t)((step + 1) * t.parts), sm.abort_flag);
+          if (ok) mbar_arrive(sm.parts_in);
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      }
+      if (!mbar_wait_warp(sm.parts_in, st.splits & 1, sm.abort_flag)) return false;
+      ++st.splits;
+    }
+    for (int32_t c = c0, j = 0; c < chunks && rows_in; c += dc, ++j, st.buf = after(st.buf, 1)) {
+      const uint32_t b = st.buf;
+      uint8_t* buf_h = bufs + b * C::kBuf;
+      uint8_t* buf_l = buf_h + 2048;
+      uint8_t* my_h = buf_h + lane * 64;
+      uint8_t* my_l = buf_l + lane * 64;
+      const int32_t col0 = t.tn * 256 + c * 32;
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(t_base + c * 32, r);
+      float dc_lane = 0.f;
+      if (kCols && col0 + lane < s.rows_b) dc_lane = __ldcg(diag + col0 + lane);
+      if (EPI == kOrthoGram) {
+        if (lane == 0) bulk_wait_group_read<C::kBufs - 1>();
+        __syncwarp();
+      } else {
+        // the next chunk's buffer, where it was not filled at the start: the
+        // store from it is the last but one
+        if (j + 1 >= C::kBufs && c + dc < chunks && lane == 0) {
+          bulk_wait_group_read<1>();
+          prefetch(c + dc, after(b, 1));
+        }
+        if (!mbar_wait_warp(&src_bar[b], (st.src_phase >> b) & 1, sm.abort_flag)) return false;
+        st.src_phase ^= 1u << b;
+      }
+      tmem_ld_wait();
+      regs_after_wait(r);
+      float v[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+      if (t.parts > 1) {
+        // the parts in order, whichever of them this one is
+        float own[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          own[e] = v[e];
+          v[e] = 0.f;
+        }
+#pragma unroll 1
+        for (int32_t k = 0; k < t.parts; ++k) {
+          const float4* d = part + (int64_t)(k - t.part) * 2 * 8 * 4 * 8 * 32 + (((int)rank * 8 + c) * 4 + sp) * 256 + lane;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = k == t.part ? make_float4(own[4 * q], own[4 * q + 1], own[4 * q + 2], own[4 * q + 3])
+                                         : __ldcg(d + q * 32);
+            v[4 * q] += f.x;
+            v[4 * q + 1] += f.y;
+            v[4 * q + 2] += f.z;
+            v[4 * q + 3] += f.w;
+          }
+        }
+      }
+      const bool on_diag = SYM && row0 == col0;  // both are multiples of 32: element `lane` of the row
+      if (EPI == kOrthoGram) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= kMScale / (kXScale * kXScale);
+        if (on_diag) {
+          float d = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e == lane) {
+              d = v[e];
+              v[e] = 0.f;
+            }
+          if (row < s.rows_a) p.diag[row] = d * (1.f / kMScale);
+        }
+      } else {
+        const float raw_scale = p.c / (kMScale * kMScale);
+        if (EPI == kOrthoPoly && on_diag) {
+          float d_new = 0.f;
+          // on the diagonal, D' = c ((O O)_ii + D_i^2) + b D_i
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e == lane) d_new = fmaf(v[e], raw_scale, dr * fmaf(p.c, dr, p.b));
+          if (row < s.rows_a) p.diag_r[row] = d_new;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 h4 = *reinterpret_cast<const uint4*>(my_h + ((q ^ sw) << 4));
+          const uint4 l4 = EPI == kOrthoUpdate ? *reinterpret_cast<const uint4*>(my_l + ((q ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+          const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int e = 8 * q + 2 * w;
+            const float2 h = half_unpack(hw[w]);
+            const float d0 = kCols ? __shfl_sync(0xFFFFFFFFu, dc_lane, e) : 0.f;
+            const float d1 = kCols ? __shfl_sync(0xFFFFFFFFu, dc_lane, e + 1) : 0.f;
+            if (EPI == kOrthoPoly) {
+              // R = c (O O + O (D_i + D_j)) + b O off the diagonal
+              v[e] = fmaf(v[e], raw_scale * kRScale, h.x * (kRScale / kMScale) * fmaf(p.c, dr + d0, p.b));
+              v[e + 1] = fmaf(v[e + 1], raw_scale * kRScale, h.y * (kRScale / kMScale) * fmaf(p.c, dr + d1, p.b));
+            } else {
+              const float2 l = half_unpack(lw[w]);
+              v[e] = fmaf(p.a + dr + d0, h.x + l.x, v[e] * (1.f / kRScale));
+              v[e + 1] = fmaf(p.a + dr + d1, h.y + l.y, v[e + 1] * (1.f / kRScale));
+            }
+          }
+        }
+        if (EPI == kOrthoPoly && on_diag) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e == lane) v[e] = 0.f;
+        }
+      }
+      if (last) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * e] * (1.f / kXScale), v[8 * q + 2 * e + 1] * (1.f / kXScale));
+            o[e] = *reinterpret_cast<uint32_t*>(&h);
+          }
+          *reinterpret_cast<uint4*>(my_h + ((q ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (!p.out_tma) {
+          // rows that do not start on 16-byte boundaries: plain stores
+          __syncwarp();
+          for (int y = 0; y < 32 && row0 + y < s.rows_a; ++y)
+            if (col0 + lane < s.rows_b)
+              p.out[(int64_t)(row0 + y) * p.ld_out + col0 + lane] = *reinterpret_cast<const __nv_bfloat16*>(
+                  buf_h + y * 64 + (((lane >> 3) ^ ((y >> 1) & 3)) << 4) + (lane & 7) * 2);
+          fence_proxy_async_smem();
+          __syncwarp();
+          continue;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 8 * q + 2 * e;
+            hi[e] = half_pair(v[i], v[i + 1]);
+            if (EPI == kOrthoUpdate) {
+              const float2 h = half_unpack(hi[e]);
+              lo[e] = half_pair(v[i] - h.x, v[i + 1] - h.y);
+            } else if (mirror) {
+              // the transposed tile beside it: rows i and i + 1, column lane
+              uint8_t* d = buf_l + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2;
+              *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(hi[e]);
+              *reinterpret_cast<uint16_t*>(d + 64) = static_cast<uint16_t>(hi[e] >> 16);
+            }
+          }
+          *reinterpret_cast<uint4*>(my_h + ((q ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (EPI == kOrthoUpdate)
+            *reinterpret_cast<uint4*>(my_l + ((q ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(dst_hi, buf_h, col0, row0);
+        if (EPI == kOrthoUpdate && !last) tma_store_2d(dst_lo, buf_l, col0, row0);
+        if (mirror) tma_store_2d(dst_hi, buf_l, row0, col0);
+        bulk_commit_group();
+      }
+    }
+    // (every TMEM read of this warp has been waited for)
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_leader<2>(&sm.acce[acc]);
+  }
+  return true;
+}
+
+template <bool TALL>
+__global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
+    ortho_kernel(const __grid_constant__ OrthoMaps m, const __grid_constant__ OrthoParams p) {
+  using C = OrthoCfg;
+  constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* empty = full + S;
-  uint64_t* accf = empty + S;
-  uint64_t* acce = accf + 2;
-  uint64_t* drain = acce + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  OrthoSmem sm;
+  sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  sm.full = reinterpret_cast<uint64_t*>(sm.base + C::kOffBar);
+  sm.empty = sm.full + S;
+  sm.accf = sm.empty + S;
+  sm.acce = sm.accf + 2;
+  sm.drain = sm.acce + 2;
+  sm.ready = sm.drain + 1;
+  sm.done = sm.ready + 1;
+  sm.parts_out = sm.done + 1;
+  sm.parts_in = sm.parts_out + 1;
+  sm.src = sm.parts_in + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.base + C::kOffMisc);
+  sm.abort_flag = reinterpret_cast<volatile int*>(sm.base + C::kOffMisc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster_id = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const int products = 3 * p.steps;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&accf[a], 1);
-      mbar_init(&acce[a], C::kEpiWarps * 2);
+      mbar_init(&sm.accf[a], 1);
+      mbar_init(&sm.acce[a], C::kEpiWarps * 2);
     }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
+    mbar_init(sm.drain, 1);
+    mbar_init(sm.ready, 1);
+    mbar_init(sm.done, C::kEpiWarps);
+    mbar_init(sm.parts_out, C::kEpiWarps);
+    mbar_init(sm.parts_in, 1);
+    for (int w = 0; w < C::kBufs * C::kEpiWarps; ++w) mbar_init(&sm.src[w], 1);
+    *sm.abort_flag = 0;
     fence_barrier_init();
-    prefetch_tmap(&tm_ah);
-    prefetch_tmap(&tm_al);
-    prefetch_tmap(&tm_bh);
-    prefetch_tmap(&tm_bl);
-    prefetch_tmap(&tm_dh);
-    prefetch_tmap(&tm_dl);
+    const CUtensorMap* maps = reinterpret_cast<const CUtensorMap*>(&m);
+    for (int i = 0; i < (int)(sizeof(OrthoMaps) / sizeof(CUtensorMap)); ++i) prefetch_tmap(maps + i);
   }
   if (warp == 1) {
     tmem_alloc<2>(tmem_slot, C::kTmemCols);
@@ -190,266 +610,108 @@ __global__ void __launch_bounds__(OrthoCfg<BN>::kThreads, 1)
   cluster_or_block_sync<2>();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_trigger();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     int stage = 0;
-    uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
-    bool ok = true;
-    for (int u = cluster_id; u < p.units && ok; u += clusters) {
-      int tm, tn;
-      ortho_tile<SYM>(p, u, tm, tn);
-      const int a0 = tm * C::kBM + 128 * (int)rank;
-      const int b0 = tn * BN + C::kBNC * (int)rank;
-      for (int i = 0; i < p.kblocks * p.passes; ++i) {
-        const int pass = i / p.kblocks, k0 = (i - pass * p.kblocks) * 64;
-        if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-        if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
-          const uint32_t bar = leader_addr<2>(&full[stage]);
-          uint8_t* da = smem + stage * C::kStageBytes;
-          uint8_t* db = da + C::kTileA;
-          const CUtensorMap* ma = pass == 2 ? &tm_al : &tm_ah;
-          const CUtensorMap* mb = pass == 1 ? &tm_bl : &tm_bh;
-          if (AMN) {
-            tma_load_2d<2>(da, ma, a0, k0, bar);
-            tma_load_2d<2>(da + 8192, ma, a0 + 64, k0, bar);
-          } else {
-            tma_load_2d<2>(da, ma, k0, a0, bar);
-          }
-          if (BMN) {
-#pragma unroll
-            for (int h = 0; h < C::kBNC / 64; ++h) tma_load_2d<2>(db + 8192 * h, mb, b0 + 64 * h, k0, bar);
-          } else {
-            tma_load_2d<2>(db, mb, k0, b0, bar);
-          }
-        }
-        issued_mask |= 1u << stage;
-        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-        if (++stage == S) { stage = 0; phase ^= 1; }
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    for (int i = 0; i < products; ++i) {
+      if (i > 0) {
+        // every CTA's results of the product before are in memory
+        bool ok = true;
+        if (lane == 0) ok = count_wait(p.grid_count, (uint32_t)i * gridDim.x, sm.abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        fence_proxy_async_all();
+        if (lane == 0) mbar_arrive(sm.ready);
       }
+      const int type = i % 3, cur = (i / 3) & 1;
+      bool ok;
+      if (type == kOrthoGram)
+        ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram[cur][0],
+                                          &m.gram[cur][1], cluster_id, clusters, rank, stage, phase, issued, issued_phase);
+      else if (type == kOrthoPoly)
+        ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o, &m.o, cluster_id, clusters, rank,
+                                            stage, phase, issued, issued_phase);
+      else if (TALL)
+        ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,
+                                             cluster_id, clusters, rank, stage, phase, issued, issued_phase);
+      else
+        ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
+                                            cluster_id, clusters, rank, stage, phase, issued, issued_phase);
+      if (!ok) break;
     }
     // let every load of the pair land before the leader can exit
     if (lane == 0 && leader) {
       for (int s = 0; s < S; ++s)
-        if (issued_mask & (1u << s)) {
+        if (issued & (1u << s)) {
           volatile int no_abort = 0;
-          mbar_wait(&full[s], (issued_phase >> s) & 1u, &no_abort, 100000000ull);
+          mbar_wait(&sm.full[s], (issued_phase >> s) & 1u, &no_abort, 100000000ull);
         }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (leader) {
-      int stage = 0, it = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const uint32_t base = smem_u32(smem);
-      const uint64_t a_desc0 = AMN ? desc_sw128_mnmajor(base) : desc_sw128_kmajor(base);
-      const uint64_t b_desc0 = BMN ? desc_sw128_mnmajor(base + C::kTileA) : desc_sw128_kmajor(base + C::kTileA);
-      constexpr uint32_t kStepA = AMN ? 2048 >> 4 : 32 >> 4;  // 16 elements along k
-      constexpr uint32_t kStepB = BMN ? 2048 >> 4 : 32 >> 4;
-      for (int u = cluster_id; u < p.units && ok; u += clusters, ++it) {
-        const int acc = it & 1;
-        if (!mbar_wait_warp(&acce[acc], ((it >> 1) & 1) ^ 1, abort_flag)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
-        for (int i = 0; i < p.kblocks * p.passes; ++i) {
-          if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t ad = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
-            const uint64_t bd = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_f16(d, ad + k * kStepA, bd + k * kStepB, kIdesc, (i | k) != 0 ? 1u : 0u);
-            tc_commit_all<2>(&empty[stage]);
-          }
-          if (++stage == S) { stage = 0; phase ^= 1; }
-        }
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      for (int i = 0; i < products; ++i) {
+        const int type = i % 3;
+        bool ok;
+        if (type == kOrthoGram)
+          ok = ortho_mma<true, TALL, TALL>(sm, p.shape[kOrthoGram], tmem, cluster_id, clusters, stage, phase, it);
+        else if (type == kOrthoPoly)
+          ok = ortho_mma<true, false, false>(sm, p.shape[kOrthoPoly], tmem, cluster_id, clusters, stage, phase, it);
+        else
+          ok = ortho_mma<false, false, !TALL>(sm, p.shape[kOrthoUpdate], tmem, cluster_id, clusters, stage, phase, it);
         if (!ok) break;
-        if (elect_one()) tc_commit_all<2>(&accf[acc]);
       }
-      if (elect_one()) tc_commit_local<2>(drain);
+      if (elect_one()) tc_commit_local<2>(sm.drain);
       volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort, 100000000ull);
+      mbar_wait(sm.drain, 0, &no_abort, 100000000ull);
       __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int sp = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* buf_h = smem + C::kOffEpi + (warp - 2) * 4096;
-    uint8_t* buf_l = buf_h + 2048;
-    constexpr int kChunks = C::kEpiCols / 32;
-    constexpr int kSrc = EPI == kOrthoUpdate ? 8 : 4;  // 16-byte words of the source per thread and chunk
-    // hands a staged pair of 32 x 32 tiles to TMA
-    auto store = [&](int x, int y, bool low) {
-      fence_proxy_async_smem();
-      __syncwarp();
+    OrthoEpiState st = {0, 0, 0, 0};
+    for (int i = 0; i < products; ++i) {
+      const int type = i % 3, step = i / 3, cur = step & 1;
+      if (i > 0 && !mbar_wait_warp(sm.ready, (uint32_t)(i - 1) & 1, sm.abort_flag)) break;
+      fence_proxy_async_all();
+      bool ok;
+      if (type == kOrthoGram)
+        ok = ortho_epilogue<kOrthoGram, TALL>(sm, p, nullptr, nullptr, &m.eo, &m.eo, tmem, cluster_id, clusters, rank,
+                                              step, st);
+      else if (type == kOrthoPoly)
+        ok = ortho_epilogue<kOrthoPoly, TALL>(sm, p, &m.eo, &m.eo, &m.er, &m.er, tmem, cluster_id, clusters, rank, step,
+                                              st);
+      else
+        ok = ortho_epilogue<kOrthoUpdate, TALL>(sm, p, &m.ex[cur][0], &m.ex[cur][1],
+                                                step == p.steps - 1 ? &m.out : &m.ex[cur ^ 1][0], &m.ex[cur ^ 1][1],
+                                                tmem, cluster_id, clusters, rank, step, st);
+      if (!ok || i == products - 1) break;
+      // this CTA's results are in memory: one arrival at the grid's barrier
       if (lane == 0) {
-        tma_store_2d(&tm_dh, buf_h, x, y);
-        if (low) tma_store_2d(&tm_dl, buf_l, x, y);
-        bulk_commit_group();
+        bulk_wait_group<0>();
+        fence_proxy_async_all();
       }
-    };
-    // waits until the buffers may be written once more
-    auto again = [&]() {
-      if (lane == 0) bulk_wait_group_read<0>();
       __syncwarp();
-    };
-    // this thread's row of a chunk of the source: O, or X hi and X lo
-    auto load_src = [&](int row, int col0, uint4 (&v)[8]) {
-      if (EPI == kOrthoGram) return;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bool in = row < p.rows_a && col0 + 8 * q < p.rows_b;
-        const int64_t at = (int64_t)row * p.ld_src + col0 + 8 * q;
-        v[q] = in ? *reinterpret_cast<const uint4*>(p.src_hi + at) : make_uint4(0, 0, 0, 0);
-        if (kSrc == 8) v[4 + q] = in ? *reinterpret_cast<const uint4*>(p.src_lo + at) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    int it = 0;
-    for (int u = cluster_id; u < p.units; u += clusters, ++it) {
-      int tm, tn;
-      ortho_tile<SYM>(p, u, tm, tn);
-      const int acc = it & 1;
-      const int row0 = tm * C::kBM + 128 * (int)rank + sp * 32;
-      const int row = row0 + lane;
-      const int colh = tn * BN + half * C::kEpiCols;
-      const bool mirror = SYM && (tn >> 1) < tm;
-      uint4 src[8];
-      load_src(row, colh, src);
-      const float dr = row < p.rows_a ? (EPI == kOrthoPoly ? p.diag[row] : EPI == kOrthoUpdate && !p.col_diag ? p.diag_r[row] : 0.f) : 0.f;
-      if (!mbar_wait_warp(&accf[acc], (it >> 1) & 1, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t t_base = tmem + ((uint32_t)(sp * 32) << 16) + acc * BN + half * C::kEpiCols;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int col0 = colh + c * 32;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t_base + c * 32, r);
-        uint4 cur[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) cur[q] = src[q];
-        if (c + 1 < kChunks) load_src(row, col0 + 32, src);
-        tmem_ld_wait();
-        regs_after_wait(r);
-        if (c == kChunks - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_leader<2>(&acce[acc]);
-        }
-        if (row0 >= p.rows_a || col0 >= p.rows_b) continue;
-        float v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-        if (EPI == kOrthoGram) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v[e] *= kMScale / (kXScale * kXScale);
-            if (row == col0 + e) {
-              if (row < p.rows_a) p.diag[row] = v[e] * (1.f / kMScale);
-              v[e] = 0.f;
-            }
-          }
-        }
-        if (EPI != kOrthoGram) {
-          // D or D' of the columns
-          const float* dp = EPI == kOrthoPoly ? p.diag : p.diag_r;
-          const float dc = (EPI == kOrthoPoly || p.col_diag) && col0 + lane < p.rows_b ? dp[col0 + lane] : 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t hw[4] = {cur[q].x, cur[q].y, cur[q].z, cur[q].w};
-            const uint32_t lw[4] = {cur[4 + q].x, cur[4 + q].y, cur[4 + q].z, cur[4 + q].w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int e = 8 * q + 2 * w;
-              const float2 h = half_unpack(hw[w]);
-              const float d0 = __shfl_sync(0xFFFFFFFFu, dc, e), d1 = __shfl_sync(0xFFFFFFFFu, dc, e + 1);
-              if (EPI == kOrthoPoly) {
-                // R = c (O O + O (D_i + D_j)) + b O off the diagonal
-                v[e] = fmaf(v[e], p.c * (kRScale / (kMScale * kMScale)), h.x * (kRScale / kMScale) * fmaf(p.c, dr + d0, p.b));
-                v[e + 1] = fmaf(v[e + 1], p.c * (kRScale / (kMScale * kMScale)), h.y * (kRScale / kMScale) * fmaf(p.c, dr + d1, p.b));
-              } else {
-                const float2 l = half_unpack(lw[w]);
-                v[e] = fmaf(p.a + dr + d0, h.x + l.x, v[e] * (1.f / kRScale));
-                v[e + 1] = fmaf(p.a + dr + d1, h.y + l.y, v[e + 1] * (1.f / kRScale));
-              }
-            }
-          }
-          if (EPI == kOrthoPoly) {
-            // on it, D' = c ((O O)_ii + D_i^2) + b D_i
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (row == col0 + e) {
-                if (row < p.rows_a)
-                  p.diag_r[row] = fmaf(__uint_as_float(r[e]), p.c / (kMScale * kMScale), dr * fmaf(p.c, dr, p.b));
-                v[e] = 0.f;
-              }
-          }
-        }
-        if (EPI == kOrthoUpdate && p.last) {
-          uint32_t o[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e] * (1.f / kXScale), v[2 * e + 1] * (1.f / kXScale));
-            o[e] = *reinterpret_cast<uint32_t*>(&h);
-          }
-          again();
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(buf_h + lane * 64 + 16 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          if (p.out_tma) {
-            store(col0, row0, false);
-          } else {
-            // rows that do not start on 16-byte boundaries: plain stores
-            __syncwarp();
-            for (int y = 0; y < 32 && row0 + y < p.rows_a; ++y)
-              if (col0 + lane < p.rows_b)
-                p.out[(int64_t)(row0 + y) * p.ld_out + col0 + lane] = reinterpret_cast<const __nv_bfloat16*>(buf_h)[y * 32 + lane];
-            __syncwarp();
-          }
-          continue;
-        }
-        uint32_t hi[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) hi[e] = half_pair(v[2 * e], v[2 * e + 1]);
-        again();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          *reinterpret_cast<uint4*>(buf_h + lane * 64 + 16 * q) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-          if (EPI == kOrthoUpdate) {
-            uint32_t lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 h = half_unpack(hi[4 * q + e]);
-              lo[e] = half_pair(v[8 * q + 2 * e] - h.x, v[8 * q + 2 * e + 1] - h.y);
-            }
-            *reinterpret_cast<uint4*>(buf_l + lane * 64 + 16 * q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        if (SYM && mirror) {
-          // the transposed tile beside it, in the second buffer
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint16_t* t = reinterpret_cast<uint16_t*>(buf_l) + 64 * e + lane;
-            t[0] = static_cast<uint16_t>(hi[e]);
-            t[32] = static_cast<uint16_t>(hi[e] >> 16);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tm_dh, buf_h, col0, row0);
-            tma_store_2d(&tm_dh, buf_l, row0, col0);
-            bulk_commit_group();
-          }
-        } else {
-          store(col0, row0, EPI == kOrthoUpdate);
-        }
+      if (lane == 0) mbar_arrive(sm.done);
+      if (warp == 2) {
+        if (!mbar_wait_warp(sm.done, (uint32_t)i & 1, sm.abort_flag)) break;
+        if (lane == 0) count_arrive(p.grid_count);
+        __syncwarp();
       }
     }
     if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+    // loads of the epilogue's inputs that a given-up wait left in flight
+    if (lane == 0 && *sm.abort_flag) {
+      for (int b = 0; b < C::kBufs; ++b)
+        for (uint32_t ph = 0; ph < 2; ++ph) {
+          volatile int no_abort = 0;
+          mbar_wait(&sm.src[(warp - 2) * C::kBufs + b], ph, &no_abort, 100000000ull);
+        }
+    }
     __syncwarp();
   }
 
@@ -470,6 +732,7 @@ struct OrthoSplitParams {
   __half* hi;
   __half* lo;
   float* part;   // [kOrthoNormBlocks]
+  uint32_t* counters;  // [kOrthoCounters], set to zero for the products
 };
 
 // Up to 8 values of a row from column c on, zeros past the end.
@@ -505,6 +768,8 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoSplitParams 
   __shared__ float sm[8];
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < kOrthoCounters; i += 256) p.counters[i] = 0u;
   float s = 0.f;
   const uint32_t per_row = (uint32_t)(p.k + 7) / 8, total = per_row * (uint32_t)p.n;
   for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {

@@ -1217,96 +1217,130 @@ namespace {
 constexpr int kOrthoMaxSteps = 64;
 constexpr int64_t kOrthoMaxDim = 65536;
 
-// An FP16 matrix [rows, cols], of X also its low terms.
-struct OrthoMat {
-  __half* hi;
-  __half* lo;
-  int64_t rows, cols, ld;
+// How the three products of a step are cut into units for 74 CTA pairs (see
+// ortho.cuh).  The tiles beyond the last full round of pairs are split along k
+// where that spares a pair at least kOrthoSpare of its 64-deep blocks; handing
+// the partials over costs about as much as six of them.
+constexpr int64_t kOrthoPairs = kSms / 2;
+constexpr int64_t kOrthoSpare = 10;
+constexpr int64_t kOrthoLeast = 4;  // blocks that a part keeps
+static_assert(kOrthoPairs <= puro::kSplitTiles, "counters for every split tile");
+
+struct OrthoPlan {
+  puro::OrthoShape shape[3];
+  int64_t pairs;        // CTA pairs of the launch
+  int64_t split_units;  // most units of split tiles in one product
 };
 
-// Where the workspace of an n x k problem keeps its matrices.
+OrthoPlan ortho_plan(int64_t n, int64_t k) {
+  OrthoPlan plan{};
+  const int64_t m = n < k ? n : k, w = n < k ? k : n;
+  const int64_t rows[3] = {m, m, n}, cols[3] = {m, m, k}, sums[3] = {w, m, m};
+  for (int i = 0; i < 3; ++i) {
+    puro::OrthoShape& s = plan.shape[i];
+    s.rows_a = (int32_t)rows[i];
+    s.rows_b = (int32_t)cols[i];
+    s.kblocks = (int32_t)((sums[i] + 63) / 64);
+    s.passes = i == puro::kOrthoGram && w <= puro::kOrthoExactK ? 3 : 1;
+    const int64_t tm = (rows[i] + 255) / 256, tn = (cols[i] + 255) / 256, total = (int64_t)s.kblocks * s.passes;
+    const int64_t tiles = i == puro::kOrthoUpdate ? tm * tn : tm * (tm + 1) / 2;
+    const int64_t rest = tiles % kOrthoPairs;
+    s.tiles_m = (int32_t)tm;
+    s.split = 1;
+    s.full = s.units = (int32_t)tiles;
+    if (rest) {
+      int64_t split = std::min<int64_t>({kOrthoPairs / rest, puro::kOrthoMaxSplit, total / kOrthoLeast});
+      if (split > 1 && total - (total + split - 1) / split >= kOrthoSpare) {
+        s.split = (int32_t)split;
+        s.full = (int32_t)(tiles - rest);
+        s.units = (int32_t)(s.full + rest * split);
+        plan.split_units = std::max(plan.split_units, rest * split);
+      }
+    }
+    plan.pairs = std::max(plan.pairs, std::min<int64_t>(s.units, kOrthoPairs));
+  }
+  return plan;
+}
+
+// Where the workspace of an n x k problem keeps its matrices, in bytes, each
+// from a multiple of 256 on.
 struct OrthoLayout {
   int64_t ld_x, ld_m;
-  int64_t x_elems, m_elems;  // FP16 elements of one matrix, a multiple of 128 (256 bytes)
+  int64_t x[2][2], o, r, diag, diag_r, part, counters, partial;
   int64_t bytes;
 };
 
-OrthoLayout ortho_layout(int64_t n, int64_t k) {
-  OrthoLayout l;
+OrthoLayout ortho_layout(int64_t n, int64_t k, const OrthoPlan& plan) {
+  OrthoLayout l{};
   const int64_t m = n < k ? n : k;
   l.ld_x = (k + 7) / 8 * 8;
   l.ld_m = (m + 7) / 8 * 8;
-  l.x_elems = (n * l.ld_x + 127) / 128 * 128;
-  l.m_elems = (m * l.ld_m + 127) / 128 * 128;
-  // two X (read and written in turn) as hi and lo; O and O'; D and D'; the norm's partial sums
-  l.bytes = (4 * l.x_elems + 2 * l.m_elems) * 2 + (2 * l.ld_m + puro::kOrthoNormBlocks) * (int64_t)sizeof(float);
+  auto take = [&](int64_t bytes) {
+    const int64_t at = l.bytes;
+    l.bytes += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  for (int i = 0; i < 2; ++i)
+    for (int t = 0; t < 2; ++t) l.x[i][t] = take(n * l.ld_x * 2);
+  l.o = take(m * l.ld_m * 2);
+  l.r = take(m * l.ld_m * 2);
+  l.diag = take(m * 4);
+  l.diag_r = take(m * 4);
+  l.part = take(puro::kOrthoNormBlocks * 4);
+  l.counters = take(puro::kOrthoCounters * 4);
+  l.partial = take(plan.split_units * 2 * 8 * 4 * 8 * 32 * 16);
   return l;
 }
 
-// One product D[i, j] = sum_k A[i, k] B[j, k] of the iteration; AMN / BMN: the
-// operand is stored [k][i] / [k][j].
-template <int BN, bool AMN, bool BMN, int EPI>
-int launch_ortho_gemm(const OrthoMat& a, const OrthoMat& b, const OrthoMat& d, puro::OrthoParams p, const DeviceInfo& dev,
-                      cudaStream_t stream) {
-  using C = puro::OrthoCfg<BN>;
-  CUtensorMap m[6];
-  int st;
-  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
-  if ((st = make_map_16(&m[0], a.hi, a.cols, a.rows, a.ld, 64, AMN ? 64 : 128, sw)) != PURO_OK) return st;
-  if ((st = make_map_16(&m[2], b.hi, b.cols, b.rows, b.ld, 64, BMN ? 64 : C::kBNC, sw)) != PURO_OK) return st;
-  m[1] = m[0];
-  m[3] = m[2];
-  if (p.passes > 1) {
-    if ((st = make_map_16(&m[1], a.lo, a.cols, a.rows, a.ld, 64, AMN ? 64 : 128, sw)) != PURO_OK) return st;
-    if ((st = make_map_16(&m[3], b.lo, b.cols, b.rows, b.ld, 64, BMN ? 64 : C::kBNC, sw)) != PURO_OK) return st;
-  }
-  m[4] = m[5] = m[0];  // not used when the result leaves by plain stores
-  if (!p.last || p.out_tma) {
-    const void* hi = p.last ? static_cast<const void*>(p.out) : d.hi;
-    if ((st = make_map_16(&m[4], hi, d.cols, d.rows, d.ld, 32, 32, none)) != PURO_OK) return st;
-    m[5] = m[4];
-    if (EPI == puro::kOrthoUpdate && !p.last &&
-        (st = make_map_16(&m[5], d.lo, d.cols, d.rows, d.ld, 32, 32, none)) != PURO_OK)
-      return st;
-  }
-  p.rows_a = (int32_t)d.rows;
-  p.rows_b = (int32_t)d.cols;
-  p.kblocks = (int32_t)(((AMN ? a.rows : a.cols) + 63) / 64);
-  p.tiles_m = (p.rows_a + C::kBM - 1) / C::kBM;
-  p.tiles_n = (p.rows_b + BN - 1) / BN;
-  if (EPI == puro::kOrthoUpdate) {
-    p.units = p.tiles_m * p.tiles_n;
-  } else {
-    p.units = 0;
-    for (int i = 0; i < p.tiles_m; ++i) p.units += 2 * i + 2 < p.tiles_n ? 2 * i + 2 : p.tiles_n;
-  }
-  auto kern = puro::ortho_gemm_kernel<BN, AMN, BMN, EPI>;
-  static std::atomic<int> max_clusters[kMaxDevices] = {};
+// Whether the FP16 form holds the iteration with these coefficients: from
+// singular values in [0, 1], X stays below 2, so that |M| <= 4, and |R| <= 15.
+bool ortho_in_range(int steps, float a, float b, float c) {
+  constexpr int kPoints = 256;
+  float x[kPoints];
+  for (int i = 0; i < kPoints; ++i) x[i] = (float)(i + 1) / kPoints;
+  bool ok = true;
+  for (int s = 0; s < steps && ok; ++s)
+    for (int i = 0; i < kPoints; ++i) {
+      const float q = x[i] * x[i], r = q * (b + c * q);
+      x[i] *= a + r;
+      ok = ok && x[i] > -2.f && x[i] < 2.f && r > -15.f && r < 15.f;
+    }
+  return ok;
+}
+
+template <bool TALL>
+int launch_ortho(const puro::OrthoMaps& m, const puro::OrthoParams& p, int64_t pairs, const DeviceInfo& dev,
+                 cudaStream_t stream) {
+  using C = puro::OrthoCfg;
+  auto kern = puro::ortho_kernel<TALL>;
+  static std::atomic<int> max_pairs[kMaxDevices] = {};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
+  attr[1].val.cooperative = 1;
+  cfg.gridDim = dim3(2 * (unsigned)kOrthoPairs);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (max_clusters[dev.index].load(std::memory_order_acquire) == 0) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-      return PURO_ERR_CUDA;
+  if (max_pairs[dev.index].load(std::memory_order_acquire) == 0) {
     int n = 0;
-    cfg.gridDim = dim3(2 * (dev.sms / 2));
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = dev.sms / 2;
-    max_clusters[dev.index].store(n, std::memory_order_release);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return PURO_ERR_CUDA;
+    }
+    max_pairs[dev.index].store(n, std::memory_order_release);
   }
-  const int most = max_clusters[dev.index].load(std::memory_order_acquire);
-  cfg.gridDim = dim3(2 * (unsigned)(p.units < most ? p.units : most));
+  if (max_pairs[dev.index].load(std::memory_order_acquire) < pairs) return PURO_ERR_UNSUPPORTED_DEVICE;
+  cfg.gridDim = dim3(2 * (unsigned)pairs);
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, m, p) != cudaSuccess) {
     cudaGetLastError();
     return PURO_ERR_CUDA;
   }
@@ -1336,7 +1370,7 @@ int launch_ortho_split(const puro::OrthoSplitParams& p, cudaStream_t stream) {
 
 extern "C" int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k) {
   if (n <= 0 || k <= 0 || n > kOrthoMaxDim || k > kOrthoMaxDim) return 0;
-  return ortho_layout(n, k).bytes;
+  return ortho_layout(n, k, ortho_plan(n, k)).bytes;
 }
 
 extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, int64_t n, int64_t k, int steps,
@@ -1345,6 +1379,7 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
   if (g_f32 & ~1) return PURO_ERR_LAYOUT;
   if (n < 0 || k < 0 || n > kOrthoMaxDim || k > kOrthoMaxDim || steps < 1 || steps > kOrthoMaxSteps || !(eps >= 0.f))
     return PURO_ERR_SHAPE;
+  if (!ortho_in_range(steps, a, b, c)) return PURO_ERR_SHAPE;
   if (n == 0 || k == 0) return PURO_OK;
   if (!g || !out || !workspace) return PURO_ERR_NULL;
   if (!aligned_to(g, g_f32 ? 4 : 2) || !aligned_to(out, 2) || !aligned_to(workspace, 256)) return PURO_ERR_ALIGN;
@@ -1355,58 +1390,56 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
   if ((st = get_encoder()) != PURO_OK) return st;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
 
-  const OrthoLayout l = ortho_layout(n, k);
+  const OrthoPlan plan = ortho_plan(n, k);
+  const OrthoLayout l = ortho_layout(n, k, plan);
   const bool tall = n > k;
   const int64_t m = tall ? k : n;
-  __half* base = static_cast<__half*>(workspace);
-  OrthoMat x[2];
-  for (int i = 0; i < 2; ++i) x[i] = OrthoMat{base + 2 * i * l.x_elems, base + (2 * i + 1) * l.x_elems, n, k, l.ld_x};
-  __half* mb = base + 4 * l.x_elems;
-  const OrthoMat mo{mb, nullptr, m, m, l.ld_m}, ro{mb + l.m_elems, nullptr, m, m, l.ld_m};
-  float* diag = reinterpret_cast<float*>(mb + 2 * l.m_elems);
-  float* diag_r = diag + l.ld_m;
+  char* ws = static_cast<char*>(workspace);
+  auto at = [&](int64_t offset) { return static_cast<void*>(ws + offset); };
+
+  // X as an operand whose sum runs along a row (K-major) or down a column
+  // (MN-major), and everything as the epilogue reads and writes it
+  puro::OrthoMaps maps;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_e = CU_TENSOR_MAP_SWIZZLE_64B;
+  for (int i = 0; i < 2; ++i) {
+    for (int t = 0; t < 2; ++t) {
+      if ((st = make_map_16(&maps.gram[i][t], at(l.x[i][t]), k, n, l.ld_x, 64, tall ? 64 : 128, sw)) != PURO_OK ||
+          (st = make_map_16(&maps.ex[i][t], at(l.x[i][t]), k, n, l.ld_x, 32, 32, sw_e)) != PURO_OK)
+        return st;
+    }
+    if ((st = make_map_16(&maps.update[i], at(l.x[i][0]), k, n, l.ld_x, 64, tall ? 128 : 64, sw)) != PURO_OK) return st;
+  }
+  if ((st = make_map_16(&maps.o, at(l.o), m, m, l.ld_m, 64, 128, sw)) != PURO_OK ||
+      (st = make_map_16(&maps.r, at(l.r), m, m, l.ld_m, 64, 128, sw)) != PURO_OK ||
+      (st = make_map_16(&maps.eo, at(l.o), m, m, l.ld_m, 32, 32, sw_e)) != PURO_OK ||
+      (st = make_map_16(&maps.er, at(l.r), m, m, l.ld_m, 32, 32, sw_e)) != PURO_OK)
+    return st;
+  const bool out_tma = aligned16(out) && ld_out % 8 == 0;
+  maps.out = maps.er;  // not used when the result leaves by plain stores
+  if (out_tma && (st = make_map_16(&maps.out, out, k, n, ld_out, 32, 32, sw_e)) != PURO_OK) return st;
+
+  puro::OrthoParams p{};
+  for (int i = 0; i < 3; ++i) p.shape[i] = plan.shape[i];
+  p.steps = steps;
+  p.a = a;
+  p.b = b;
+  p.c = c;
+  p.diag = static_cast<float*>(at(l.diag));
+  p.diag_r = static_cast<float*>(at(l.diag_r));
+  p.grid_count = static_cast<uint32_t*>(at(l.counters));
+  p.tile_count = p.grid_count + 64;
+  p.partial = static_cast<float4*>(at(l.partial));
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ld_out = ld_out;
+  p.out_tma = out_tma;
 
   const bool vec = aligned16(g) && ld_g % (g_f32 ? 4 : 8) == 0;
-  const puro::OrthoSplitParams sp{g, ld_g, l.ld_x, (int32_t)n, (int32_t)k, eps, x[0].hi, x[0].lo, diag_r + l.ld_m};
+  const puro::OrthoSplitParams sp{g, ld_g, l.ld_x, (int32_t)n, (int32_t)k, eps, static_cast<__half*>(at(l.x[0][0])),
+                                  static_cast<__half*>(at(l.x[0][1])), static_cast<float*>(at(l.part)), p.grid_count};
   if (g_f32)
     st = vec ? launch_ortho_split<true, true>(sp, sm) : launch_ortho_split<true, false>(sp, sm);
   else
     st = vec ? launch_ortho_split<false, true>(sp, sm) : launch_ortho_split<false, false>(sp, sm);
   if (st != PURO_OK) return st;
-
-  for (int i = 0; i < steps; ++i) {
-    const OrthoMat &cur = x[i & 1], &next = x[(i + 1) & 1];
-    puro::OrthoParams p{};
-    p.a = a;
-    p.b = b;
-    p.c = c;
-    p.diag = diag;
-    p.diag_r = diag_r;
-    puro::OrthoParams pg = p;
-    pg.passes = (tall ? n : k) <= puro::kOrthoExactK ? 3 : 1;
-    st = tall ? launch_ortho_gemm<128, true, true, puro::kOrthoGram>(cur, cur, mo, pg, *dev, sm)
-              : launch_ortho_gemm<128, false, false, puro::kOrthoGram>(cur, cur, mo, pg, *dev, sm);
-    if (st != PURO_OK) return st;
-    p.passes = 1;
-    p.src_hi = mo.hi;
-    p.ld_src = mo.ld;
-    st = launch_ortho_gemm<128, false, false, puro::kOrthoPoly>(mo, mo, ro, p, *dev, sm);
-    if (st != PURO_OK) return st;
-    p.src_hi = cur.hi;
-    p.src_lo = cur.lo;
-    p.ld_src = cur.ld;
-    p.col_diag = tall;
-    OrthoMat d = next;
-    if (i == steps - 1) {
-      p.last = 1;
-      p.out = static_cast<__nv_bfloat16*>(out);
-      p.ld_out = ld_out;
-      p.out_tma = aligned16(out) && ld_out % 8 == 0;
-      d.ld = ld_out;
-    }
-    st = tall ? launch_ortho_gemm<256, false, false, puro::kOrthoUpdate>(cur, ro, d, p, *dev, sm)
-              : launch_ortho_gemm<256, false, true, puro::kOrthoUpdate>(ro, cur, d, p, *dev, sm);
-    if (st != PURO_OK) return st;
-  }
-  return PURO_OK;
+  return tall ? launch_ortho<true>(maps, p, plan.pairs, *dev, sm) : launch_ortho<false>(maps, p, plan.pairs, *dev, sm);
 }
