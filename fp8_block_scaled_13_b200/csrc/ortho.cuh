@@ -30,8 +30,9 @@
 // the two FP16 terms of X0).  Its 3 * steps products D[i, j] = sum_k A[i, k]
 // B[j, k] follow each other over a barrier of the grid's CTAs: the next
 // product's loads wait for it, everything else (TMEM, barriers, tensor maps)
-// stays set up.  (One launch per product cost 3.8 us each in tails and starts:
-// @)
+// stays set up.  (One launch per product took 3.8 us each in tails and starts;
+// with 128-column tiles and without the split below: 313 us against 267 for
+// 2048 x 2048, 1133 against 800 to 950, by the power cap, for 12288 x 2048.)
 //
 // A product runs tcgen05 kind::f16 on CTA pairs, 256 x 256 tiles, FP32
 // accumulators in TMEM (two, so that a tile's epilogue overlaps the next one's
@@ -60,7 +61,7 @@ namespace puro {
 
 enum OrthoProduct : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2 };
 
-constexpr int kOrthoNormBlocks = 592;  // CTAs of the norm pass, one partial sum each
+constexpr int kOrthoNormBlocks = 592;  // most CTAs of the passes over G, one partial sum each
 constexpr int64_t kOrthoExactK = 1024; // longest X X^T sum that takes three products
 constexpr float kXScale = 1024.f, kMScale = 8192.f, kRScale = 4096.f;
 constexpr int kOrthoMaxSplit = 8;
@@ -71,7 +72,7 @@ struct OrthoShape {
   int32_t rows_a, rows_b;   // D is [rows_a, rows_b]
   int32_t kblocks;          // ceil(K / 64)
   int32_t passes;           // 1: hi hi; 3: hi hi, hi lo, lo hi
-  int32_t tiles_m;          // kOrthoUpdate: tiles down (the others count the lower triangle)
+  int32_t tiles_m, tiles_n; // kOrthoUpdate (the others count the lower triangle)
   int32_t full, split, units;
 };
 
@@ -83,11 +84,12 @@ struct OrthoParams {
   float* diag_r;            // D', the diagonal of R
   uint32_t* grid_count;     // arrivals at the grid barrier; zero before the launch
   uint32_t* tile_count;     // [3][kSplitTiles][2] arrivals of a split tile's parts; zero before the launch
-  float4* partial;          // [units of split tiles][2][8][4][8][32]
+  float4* partial;          // [units of split tiles][kPartial]
   __nv_bfloat16* out;       // the BF16 result, by plain stores if out_tma is 0
   int64_t ld_out;
   int32_t out_tma;
 };
+constexpr int kPartial = 2 * 8 * 4 * 8 * 32;  // float4 of a tile's partials: [CTA][chunk][32 rows][8][lane]
 constexpr int kSplitTiles = 74;  // most tiles that can be split: fewer than CTA pairs
 constexpr int kOrthoCounters = 64 + 3 * kSplitTiles * 2;
 
@@ -169,8 +171,15 @@ __device__ __forceinline__ OrthoUnit ortho_unit(const OrthoShape& s, int32_t u) 
     r.tm = i;
     r.tn = t;
   } else {
-    r.tn = t / s.tiles_m;
-    r.tm = t - r.tn * s.tiles_m;
+    // along the shorter side of D first, so that tiles that run at the same
+    // time share their part of X
+    if (s.tiles_n < s.tiles_m) {
+      r.tm = t / s.tiles_n;
+      r.tn = t - r.tm * s.tiles_n;
+    } else {
+      r.tn = t / s.tiles_m;
+      r.tm = t - r.tn * s.tiles_m;
+    }
   }
   const int32_t left = s.rows_b - r.tn * 256;
   r.cols = left >= 256 ? 256 : (left + 31) / 32 * 32;
@@ -356,10 +365,16 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
     }
     float dr = 0.f;
     if (row < s.rows_a && (EPI == kOrthoPoly || (EPI == kOrthoUpdate && !TALL))) dr = __ldcg(diag + row);
+    // the diagonal at a chunk's columns, one per lane
+    auto load_diag = [&](int32_t c) {
+      const int32_t x = t.tn * 256 + c * 32 + lane;
+      return kCols && c < chunks && x < s.rows_b ? __ldcg(diag + x) : 0.f;
+    };
+    float d_next = load_diag(c0);
     if (!mbar_wait_warp(&sm.accf[acc], (st.it >> 1) & 1, sm.abort_flag)) return false;
     tc_fence_after();
     const uint32_t t_base = tmem + ((uint32_t)(sp * 32) << 16) + acc * 256;
-    float4* part = p.partial + (int64_t)(u - s.full) * 2 * 8 * 4 * 8 * 32;
+    float4* part = p.partial + (int64_t)(u - s.full) * kPartial;
     if (t.parts > 1) {
       // the chunks that other parts own leave as FP32
       for (int32_t c = half; c < chunks && rows_in; c += 2) {
@@ -399,8 +414,8 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
       const int32_t col0 = t.tn * 256 + c * 32;
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_base + c * 32, r);
-      float dc_lane = 0.f;
-      if (kCols && col0 + lane < s.rows_b) dc_lane = __ldcg(diag + col0 + lane);
+      const float dc_lane = d_next;
+      d_next = load_diag(c + dc);
       if (EPI == kOrthoGram) {
         if (lane == 0) bulk_wait_group_read<C::kBufs - 1>();
         __syncwarp();
@@ -419,26 +434,18 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
       float v[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-      if (t.parts > 1) {
-        // the parts in order, whichever of them this one is
-        float own[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          own[e] = v[e];
-          v[e] = 0.f;
-        }
+      // the other parts, in an order that depends on the chunk alone (its owner)
 #pragma unroll 1
-        for (int32_t k = 0; k < t.parts; ++k) {
-          const float4* d = part + (int64_t)(k - t.part) * 2 * 8 * 4 * 8 * 32 + (((int)rank * 8 + c) * 4 + sp) * 256 + lane;
+      for (int32_t k = 1; k < t.parts; ++k) {
+        const int32_t other = t.part + k < t.parts ? k : k - t.parts;
+        const float4* d = part + (int64_t)other * kPartial + (((int)rank * 8 + c) * 4 + sp) * 256 + lane;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 f = k == t.part ? make_float4(own[4 * q], own[4 * q + 1], own[4 * q + 2], own[4 * q + 3])
-                                         : __ldcg(d + q * 32);
-            v[4 * q] += f.x;
-            v[4 * q + 1] += f.y;
-            v[4 * q + 2] += f.z;
-            v[4 * q + 3] += f.w;
-          }
+        for (int q = 0; q < 8; ++q) {
+          const float4 f = __ldcg(d + q * 32);
+          v[4 * q] += f.x;
+          v[4 * q + 1] += f.y;
+          v[4 * q + 2] += f.z;
+          v[4 * q + 3] += f.w;
         }
       }
       const bool on_diag = SYM && row0 == col0;  // both are multiples of 32: element `lane` of the row
@@ -731,7 +738,7 @@ struct OrthoSplitParams {
   float eps;
   __half* hi;
   __half* lo;
-  float* part;   // [kOrthoNormBlocks]
+  float* part;   // one per CTA (both passes have the same grid)
   uint32_t* counters;  // [kOrthoCounters], set to zero for the products
 };
 
@@ -796,7 +803,7 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const OrthoSplitParams
   pdl_wait();
   pdl_trigger();
   float s = 0.f;  // every warp adds the partial sums in the same order
-  for (int i = threadIdx.x & 31; i < kOrthoNormBlocks; i += 32) s += p.part[i];
+  for (int i = threadIdx.x & 31; i < (int)gridDim.x; i += 32) s += p.part[i];
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
   const float scale = kXScale / (sqrtf(s) + p.eps);

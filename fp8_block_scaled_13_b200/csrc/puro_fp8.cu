@@ -1246,6 +1246,7 @@ OrthoPlan ortho_plan(int64_t n, int64_t k) {
     const int64_t tiles = i == puro::kOrthoUpdate ? tm * tn : tm * (tm + 1) / 2;
     const int64_t rest = tiles % kOrthoPairs;
     s.tiles_m = (int32_t)tm;
+    s.tiles_n = (int32_t)tn;
     s.split = 1;
     s.full = s.units = (int32_t)tiles;
     if (rest) {
@@ -1288,7 +1289,7 @@ OrthoLayout ortho_layout(int64_t n, int64_t k, const OrthoPlan& plan) {
   l.diag_r = take(m * 4);
   l.part = take(puro::kOrthoNormBlocks * 4);
   l.counters = take(puro::kOrthoCounters * 4);
-  l.partial = take(plan.split_units * 2 * 8 * 4 * 8 * 32 * 16);
+  l.partial = take(plan.split_units * puro::kPartial * 16);
   return l;
 }
 
@@ -1353,7 +1354,8 @@ int launch_ortho_split(const puro::OrthoSplitParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(puro::kOrthoNormBlocks);
+  const int64_t pieces = (int64_t)p.n * ((p.k + 7) / 8);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(puro::kOrthoNormBlocks, (pieces + 255) / 256));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
