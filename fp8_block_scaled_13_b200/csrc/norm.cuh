@@ -27,7 +27,7 @@
 // than one pass would have to, but each streams without a pause: a single
 // kernel on clusters of 8 CTAs x 16 rows, which held the rows in shared memory
 // and exchanged column maxima, spent most of its time in barriers with no load
-// in flight (32768 x 2048 on both norms: 227 us forward and 347 us backward, against 124 us and 232 us now).
+// in flight (32768 x 2048 on both norms: 227 us forward and 347 us backward, against 119 us and 226 us now).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -556,6 +556,7 @@ struct NormColumnParams {
   int32_t w_f32, gate_f32;
   float scale;
   int32_t accumulate;
+  int32_t early;      // see below
   float* dw_pre;
   float* dw_post;     // or null
   float* dgate;       // channel gate's gradient or null
@@ -565,14 +566,19 @@ __global__ void __launch_bounds__(512) norm_column_kernel(const NormColumnParams
   __shared__ float sm[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t c = blockIdx.x * 32 + lane;  // cols is a multiple of 128
-  pdl_wait();
+  // early: the quantizer runs between the row pass and this one.  Its CTAs let
+  // this kernel start only once they have seen the row pass complete, so the
+  // sums may be read while it still works; the wait for it comes at the end,
+  // so that whatever waits for this kernel has waited for both.
+  if (!p.early) pdl_wait();
   pdl_trigger();
   float a = 0.f;
   const float* src = p.part + (int64_t)blockIdx.y * p.cols + c;
 #pragma unroll 8
-  for (int64_t i = warp; i < p.parts; i += 16) a += src[i * 2 * p.cols];
+  for (int64_t i = warp; i < p.parts; i += 16) a += __ldcg(src + i * 2 * p.cols);
   sm[warp][lane] = a;
   __syncthreads();
+  if (p.early) pdl_wait();
   if (warp) return;
 #pragma unroll
   for (int k = 1; k < 16; ++k) a += sm[k][lane];
