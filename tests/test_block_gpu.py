@@ -215,3 +215,104 @@ def test_swiglu_backward(fp8, oracle_mod, t, f):
     for layout in ("rowwise", "colwise", "both"):
         _same_codes(fp8.swiglu_backward(da, gu, layout=layout), d, oracle_mod, layout)
     assert fp8.device_status() == 0
+
+
+def test_backward_offsets_past_32_bits(fp8):
+    """Over 2^31 elements: the last rows' gradients come out as they do by themselves."""
+    t, d = 1_060_000, 2048
+    x = torch.zeros(t, d, dtype=torch.bfloat16, device="cuda")
+    x[-130:] = _bf((130, d), 1)
+    dn = torch.zeros(t, d, dtype=torch.bfloat16, device="cuda")
+    dn[-130:] = _bf((130, d), 2)
+    w = torch.ones(d, device="cuda")
+    f = fp8.residual_norm(x, w, layout="bf16")
+    big = fp8.residual_norm_backward(dn, x, f.rstd, w, layout="bf16")
+    small = fp8.residual_norm_backward(dn[-130:].clone(), x[-130:].clone(), f.rstd[-130:].clone(), w, layout="bf16")
+    assert torch.equal(big.dx[-130:], small.dx) and torch.allclose(big.dw_pre, small.dw_pre, rtol=1e-4, atol=1e-3)
+    del f, big, x, dn
+    t, f = 180_000, 6144
+    gu = torch.zeros(t, 2 * f, dtype=torch.bfloat16, device="cuda")
+    gu[-130:] = _bf((130, 2 * f), 3)
+    # (a group of transposed codes is 128 rows from the start: 180000 = 1406 * 128 + 32)
+    a, b = fp8.swiglu(gu), fp8.swiglu(gu[-160:].clone())
+    assert torch.equal(a.q[-160:], b.q) and torch.equal(a.qt[:, t - 160:], b.qt[:, :160])
+
+
+@pytest.mark.parametrize("t,d", [(70, 384), (300, 2176), (129, 4224)])
+def test_norm_weights_off_16_byte_boundaries(fp8, t, d):
+    torch.manual_seed(t)
+    x, _, h, _ = _inputs(t, d, True, True, None, True, t)
+    dn = _bf((t, d), 9)
+    for wt in (torch.float32, torch.bfloat16):
+        w, wp, gate = [(1 + 0.2 * torch.randn(d, device="cuda")).to(wt) for _ in range(3)]
+        off = [torch.cat([v[:1], v])[1:] for v in (w, wp, gate)]   # one element into their memory
+        assert all(v.data_ptr() % 16 for v in off)
+        a = fp8.residual_norm(x, w, h, w_post=wp, gate=gate[None])
+        b = fp8.residual_norm(x, off[0], h, w_post=off[1], gate=off[2][None])
+        assert torch.equal(a.y, b.y) and torch.equal(a.n.q, b.n.q) and torch.equal(a.n.qt, b.n.qt)
+        kw = dict(rstd_post=a.rstd_post)
+        ga = fp8.residual_norm_backward(dn, a.y, a.rstd, w, h, w_post=wp, gate=gate[None], **kw)
+        gb = fp8.residual_norm_backward(dn, a.y, a.rstd, off[0], h, w_post=off[1], gate=off[2][None], **kw)
+        for n in ("dx", "dw_pre", "dw_post", "dgate"):
+            assert torch.equal(getattr(ga, n), getattr(gb, n)), n
+        assert torch.equal(ga.dh.qt, gb.dh.qt)
+
+
+def test_a_token_does_not_see_its_neighbours(fp8):
+    """A token's result is the same alone and in a batch, and one that is not a number stays by itself."""
+    for d in (256, 2048, 4224):
+        x, h = _bf((700, d), d), _bf((700, d), d + 1)
+        w = 1 + 0.2 * torch.randn(d, device="cuda")
+        r = fp8.residual_norm(x, w, h, w_post=w, layout="bf16")
+        for i in (0, 15, 16, 333, 699):
+            one = fp8.residual_norm(x[i:i + 1], w, h[i:i + 1], w_post=w, layout="bf16")
+            assert torch.equal(one.n[0], r.n[i]) and torch.equal(one.y[0], r.y[i])
+        x[333] = float("nan")
+        bad = fp8.residual_norm(x, w, h, w_post=w, layout="bf16")
+        keep = torch.arange(700, device="cuda") != 333
+        assert torch.equal(bad.n[keep], r.n[keep]) and bad.n[333].isnan().all()
+
+
+def test_only_the_results_are_written(fp8):
+    """Wider buffers: what lies beside the results keeps its bytes."""
+    t, d = 150, 384
+    x, h, dn, gu = _bf((t, d), 1), _bf((t, d), 2), _bf((t, d), 3), _bf((t, 2 * d), 4)
+    w = torch.ones(d, device="cuda")
+
+    def buffers(cols):
+        q = torch.full((t + 9, cols + 32), 9, dtype=torch.uint8, device="cuda")
+        qt = torch.full((cols + 3, 160 + 48), 9, dtype=torch.uint8, device="cuda")
+        fresh = fp8.quant_act(torch.zeros(t, cols, dtype=torch.bfloat16, device="cuda"))
+        return q, qt, fp8.QuantAct(t, cols, q=q[:t, :cols], s=fresh.s, qt=qt[:cols, :160], st=fresh.st)
+
+    def check(q, qt, cols):
+        assert (q[t:] == 9).all() and (q[:, cols:] == 9).all() and (qt[cols:] == 9).all() and (qt[:, 160:] == 9).all()
+
+    wide = [torch.full((t + 5, d + 64), -3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    q, qt, out = buffers(d)
+    r = fp8.residual_norm(x, w, h, y=wide[0][:t, :d], out=out)
+    check(q, qt, d)
+    q, qt, out = buffers(d)
+    fp8.residual_norm_backward(dn, r.y, r.rstd, w, h, dx=wide[1][:t, :d], out=out)
+    check(q, qt, d)
+    for v in wide:
+        assert (v[t:] == -3).all() and (v[:, d:] == -3).all()
+    q, qt, out = buffers(d)
+    fp8.swiglu(gu, out=out)
+    check(q, qt, d)
+    q, qt, out = buffers(2 * d)
+    fp8.swiglu_backward(dn, gu, out=out)
+    check(q, qt, 2 * d)
+
+
+def test_repeatable(fp8):
+    """Sums over tokens are added in a fixed order, whatever CTA takes which rows or tile."""
+    t, d = 5000, 2048
+    x, h, dn = _bf((t, d), 1), _bf((t, d), 2), _bf((t, d), 3)
+    w = 1 + 0.1 * torch.randn(d, device="cuda")
+    f = fp8.residual_norm(x, w, h, w_post=w)
+    one = fp8.residual_norm_backward(dn, f.y, f.rstd, w, h, w_post=w, rstd_post=f.rstd_post)
+    for _ in range(5):
+        r = fp8.residual_norm_backward(dn, f.y, f.rstd, w, h, w_post=w, rstd_post=f.rstd_post)
+        assert torch.equal(r.dw_pre, one.dw_pre) and torch.equal(r.dw_post, one.dw_post)
+        assert torch.equal(r.dh.q, one.dh.q) and torch.equal(r.dh.qt, one.dh.qt)

@@ -59,3 +59,101 @@ def test_orthogonalize(fp8, n, k, dtype):
     got = fp8.orthogonalize(g)
     assert fp8.device_status() == 0
     assert got.dtype == torch.bfloat16 and _error(got, _reference(g)) <= BOUND
+
+
+@pytest.mark.parametrize("n,k", [(257, 300), (300, 257), (640, 512), (1280, 2300), (2300, 1280)])
+def test_any_strides_and_alignment(fp8, n, k):
+    """Views that start and step off 16-byte boundaries give what aligned copies give, and nothing beside them is written."""
+    for dtype in (torch.float32, torch.bfloat16):
+        g = _gradient(n, k, n + k, dtype)
+        want = fp8.orthogonalize(g)
+        for shift, pad in ((0, 8), (1, 3), (3, 5)):
+            wide = torch.full((n, k + shift + pad), float("nan"), dtype=dtype, device="cuda")
+            wide[:, shift:shift + k] = g
+            out = torch.full((n, k + shift + pad), -7.0, dtype=torch.bfloat16, device="cuda")
+            got = fp8.orthogonalize(wide[:, shift:shift + k], out=out[:, shift:shift + k])
+            assert torch.equal(got, want)
+            assert (out[:, :shift] == -7).all() and (out[:, shift + k:] == -7).all()
+
+
+# every way a product is cut: one tile; rounds of whole tiles; the rest split; three products or one for X X^T
+@pytest.mark.parametrize("n,k", [(256, 256), (512, 2048), (1536, 1536), (2048, 1024), (2560, 2048), (300, 5000), (5000, 300),
+                                 (4100, 2050)])
+def test_tile_schedules_and_repeatability(fp8, n, k):
+    g = _gradient(n, k, 5, torch.float32)
+    got = fp8.orthogonalize(g)
+    assert _error(got, _reference(g)) <= BOUND
+    for _ in range(3):
+        assert torch.equal(fp8.orthogonalize(g), got)
+    assert fp8.device_status() == 0
+
+
+def test_spectra(fp8):
+    """Low rank over a floor, a power law, a geometric fall over two decades, one strong direction: a floor or a
+    smallest value of 1 / 100 of the strongest direction, five times less than the bound's inputs; the roundings of
+    X X^T then enter five times more, 2.26e-3 + 5 * 1.6e-3."""
+    t = torch.Generator(device="cuda").manual_seed(3)
+    n, k = 256, 768
+    q1, _ = torch.linalg.qr(torch.randn(n, n, generator=t, device="cuda", dtype=torch.float64))
+    q2, _ = torch.linalg.qr(torch.randn(k, n, generator=t, device="cuda", dtype=torch.float64))
+    i = torch.arange(n, device="cuda", dtype=torch.float64)
+    for s in (1 / (1 + i) + 0.01, 10 ** (-2 * i / n), (i < 16) + 0.05, (i < 1) + 0.02):
+        g = (q1 * s) @ q2.T
+        assert _error(fp8.orthogonalize(g.float()), _reference(g.float())) <= 2.26e-3 + 5 * 1.6e-3
+
+
+@pytest.mark.parametrize("steps", [1, 2, 10])
+def test_steps_and_coefficients(fp8, steps):
+    for coefficients in (NS, (2.0, -1.5, 0.5), (1.875, -1.25, 0.375)):
+        g = _gradient(200, 520, steps, torch.float32)
+        got = fp8.orthogonalize(g, steps=steps, coefficients=coefficients)
+        # six roundings of 2.8e-4 a step
+        bound = 2.26e-3 + (6 * steps) ** 0.5 * 2.8e-4 * 2
+        assert _error(got, _reference(g, steps, 1e-7, coefficients)) <= bound
+
+
+def test_size_of_the_gradient(fp8):
+    """The result does not depend on the gradient's size (eps is far below it), and a zero gradient gives zero."""
+    g = _gradient(320, 512, 1, torch.float32, size=1.0)
+    want = _reference(g)
+    for size in (1e-12, 1e-3, 1e6, 1e15):
+        assert _error(fp8.orthogonalize(g * size, eps=0.0 if size < 1e-6 else 1e-7), want) <= BOUND
+    assert not fp8.orthogonalize(torch.zeros(320, 512, device="cuda")).any()
+    # a gradient below eps: X0 is small, and five steps lift it by at most 3.4445 each
+    small = g / g.norm() * 1e-5
+    assert _error(fp8.orthogonalize(small, eps=1e-3), _reference(small, eps=1e-3)) <= BOUND
+    for shape in ((0, 5), (5, 0)):
+        assert fp8.orthogonalize(torch.empty(shape, device="cuda")).shape == shape
+
+
+def test_streams_workspaces_and_graphs(fp8):
+    from fp8_block_scaled_13_b200 import _lib
+    gs = [_gradient(600 + 40 * i, 1100, i, torch.float32) for i in range(4)]
+    want = [fp8.orthogonalize(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    torch.cuda.synchronize()
+    got = [None] * 4
+    for _ in range(3):   # calls that may run at the same time
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = fp8.orthogonalize(gs[i])
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    # two captured calls on one workspace, whatever it held before, and inputs that change between replays
+    ws = torch.full((max(_lib.puro_fp8_orthogonalize_workspace_bytes(*g.shape) for g in gs),), 255, dtype=torch.uint8,
+                    device="cuda")
+    g, out = [x.clone() for x in gs[:2]], [torch.empty_like(w) for w in want[:2]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(2):
+            fp8.orthogonalize(g[i], out=out[i], workspace=ws)
+    for flip in (1.0, -1.0):
+        for i in range(2):
+            g[i].copy_(gs[i] * flip)
+        ws.fill_(77)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(out[i], want[i] * flip)
+    assert fp8.device_status() == 0
