@@ -34,19 +34,20 @@
 // with 128-column tiles and without the split below: 313 us against 267 for
 // 2048 x 2048, 1133 against 800 to 950, by the power cap, for 12288 x 2048.)
 //
-// A product runs tcgen05 kind::f16 on CTA pairs, 256 x 256 tiles, FP32
-// accumulators in TMEM (two, so that a tile's epilogue overlaps the next one's
-// products), fed by TMA through a ring of 64-deep stages.  256 columns let the
-// loads (64 bytes a clock and SM at the full rate) just follow the tensor
-// cores; 128 columns need 96 and got 0.57 of the rate.  An operand that is
-// stored the other way round ([k][i]) is read MN-major, so nothing is ever
-// transposed in memory.  M and R are symmetric: only tiles on or below the
-// diagonal are computed, and the epilogue writes each one also to its mirrored
-// place.  The tiles that do not fill a round of all CTA pairs are split along
-// k over the idle pairs; each of them leaves the FP32 partials that it does not
-// own in the workspace, waits for the others' and finishes its own share of the
-// columns, so the epilogue is split as well.  (2048 x 2048: 36 tiles of M
-// become 72 half tiles on 74 pairs.)
+// A product runs tcgen05 kind::f16 on CTA pairs, in tiles of 256 rows and 256,
+// 128 or 64 columns, FP32 accumulators in TMEM (two, so that a tile's epilogue
+// overlaps the next one's products), fed by TMA through a ring of 64-deep
+// stages.  256 columns let the loads (64 bytes a clock and SM at the full rate)
+// just follow the tensor cores; 128 columns need 96 and got 0.57 of the rate
+// on all SMs, but a small product is done sooner in narrow tiles on more of
+// them, each with less of an epilogue.  An operand that is stored the other way
+// round ([k][i]) is read MN-major, so nothing is ever transposed in memory.  M
+// and R are symmetric: only tiles that reach the diagonal's 256 x 256 blocks or
+// lie below are computed, and the epilogue writes those below also to their
+// mirrored place.  The tiles that do not fill a round of all CTA pairs may be
+// split along k over the idle pairs; each of them leaves the FP32 partials that
+// it does not own in the workspace, waits for the others' and finishes its own
+// share of the columns, so the epilogue is split as well.
 // The epilogue's own inputs (O, or both terms of X) come by TMA into the buffer
 // that the result then leaves from, a chunk of 32 x 32 ahead.  Bound by the
 // tensor cores for large G, by the 3 * steps hand-overs for small ones.
@@ -72,7 +73,8 @@ struct OrthoShape {
   int32_t rows_a, rows_b;   // D is [rows_a, rows_b]
   int32_t kblocks;          // ceil(K / 64)
   int32_t passes;           // 1: hi hi; 3: hi hi, hi lo, lo hi
-  int32_t tiles_m, tiles_n; // kOrthoUpdate (the others count the lower triangle)
+  int32_t bn;               // columns of a tile: 256, 128 or 64 (its rows are 256)
+  int32_t tiles_m, tiles_n;
   int32_t full, split, units;
 };
 
@@ -93,12 +95,14 @@ constexpr int kPartial = 2 * 8 * 4 * 8 * 32;  // float4 of a tile's partials: [C
 constexpr int kSplitTiles = 74;  // most tiles that can be split: fewer than CTA pairs
 constexpr int kOrthoCounters = 64 + 3 * kSplitTiles * 2;
 
-// Tensor maps.  Operands: 64-wide boxes with the 128-byte swizzle, 128 rows
-// (K-major) or 64 (MN-major); epilogue: boxes of 32 x 32 with the 64-byte one.
+// Tensor maps.  Operands: 64-wide boxes with the 128-byte swizzle, 64 rows if
+// MN-major, else 128 rows (A) or half a tile's columns (B); epilogue: boxes of
+// 32 x 32 with the 64-byte swizzle.
 struct OrthoMaps {
-  CUtensorMap gram[2][2];   // X as the operands of X X^T: [buffer][hi, lo]
-  CUtensorMap update[2];    // X hi as an operand of the update
-  CUtensorMap o, r;         // O (both operands of the square), R (an operand of the update)
+  CUtensorMap gram[2][2], gram_b[2][2];  // X as the operands of X X^T: [buffer][hi, lo]
+  CUtensorMap update[2];                 // X hi as an operand of the update
+  CUtensorMap o, o_b;                    // O, both operands of the square
+  CUtensorMap r;                         // R, an operand of the update
   CUtensorMap ex[2][2], eo, er, out;
 };
 
@@ -141,8 +145,8 @@ __device__ __forceinline__ uint64_t desc_sw128_mnmajor(uint32_t saddr) {
 }
 
 struct OrthoUnit {
-  int32_t tm, tn;       // 256 x 256 tile
-  int32_t cols;         // columns of D that it computes: a multiple of 32, 256 at most
+  int32_t y0, x0;       // the tile's first row and column of D
+  int32_t cols;         // columns of D that it computes: a multiple of 32, bn at most
   int32_t k0, k1;       // its 64-deep blocks, of kblocks * passes
   int32_t part, parts;  // its place among the parts of a split tile
   int32_t index;        // of the split tile
@@ -164,25 +168,28 @@ __device__ __forceinline__ OrthoUnit ortho_unit(const OrthoShape& s, int32_t u) 
   }
   r.k0 = (int32_t)((int64_t)total * r.part / r.parts);
   r.k1 = (int32_t)((int64_t)total * (r.part + 1) / r.parts);
+  int32_t tm, tn;
   if (SYM) {
-    // row by row of the lower triangle
-    int32_t i = 0;
-    for (; t > i; ++i) t -= i + 1;
-    r.tm = i;
-    r.tn = t;
-  } else {
+    // row by row of tiles that reach the diagonal's 256 x 256 blocks or lie below
+    for (tm = 0;; ++tm) {
+      const int32_t to_diag = (tm + 1) * (256 / s.bn), n = to_diag < s.tiles_n ? to_diag : s.tiles_n;
+      if (t < n) break;
+      t -= n;
+    }
+    tn = t;
+  } else if (s.tiles_n < s.tiles_m) {
     // along the shorter side of D first, so that tiles that run at the same
     // time share their part of X
-    if (s.tiles_n < s.tiles_m) {
-      r.tm = t / s.tiles_n;
-      r.tn = t - r.tm * s.tiles_n;
-    } else {
-      r.tn = t / s.tiles_m;
-      r.tm = t - r.tn * s.tiles_m;
-    }
+    tm = t / s.tiles_n;
+    tn = t - tm * s.tiles_n;
+  } else {
+    tn = t / s.tiles_m;
+    tm = t - tn * s.tiles_m;
   }
-  const int32_t left = s.rows_b - r.tn * 256;
-  r.cols = left >= 256 ? 256 : (left + 31) / 32 * 32;
+  r.y0 = tm * 256;
+  r.x0 = tn * s.bn;
+  const int32_t left = s.rows_b - r.x0;
+  r.cols = left >= s.bn ? s.bn : (left + 31) / 32 * 32;
   return r;
 }
 
@@ -234,15 +241,17 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
                                            int cluster_id, int clusters, uint32_t rank, int& stage, uint32_t& phase,
                                            uint32_t& issued, uint32_t& issued_phase) {
   using C = OrthoCfg;
+  // both CTAs' bytes of a stage
+  const uint32_t bytes = 2 * (C::kTile + (BMN ? (s.bn == 256 ? 16384u : 8192u) : (uint32_t)s.bn * 64));
   for (int32_t u = cluster_id; u < s.units; u += clusters) {
     const OrthoUnit t = ortho_unit<SYM>(s, u);
-    const int32_t a0 = t.tm * 256 + 128 * (int32_t)rank;
-    const int32_t b0 = t.tn * 256 + (t.cols >> 1) * (int32_t)rank;
+    const int32_t a0 = t.y0 + 128 * (int32_t)rank;
+    const int32_t b0 = t.x0 + (t.cols >> 1) * (int32_t)rank;
     for (int32_t i = t.k0; i < t.k1; ++i) {
       const int32_t pass = s.passes == 1 ? 0 : i / s.kblocks, k = (i - pass * s.kblocks) * 64;
       if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1, sm.abort_flag)) return false;
       if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], 2 * C::kStageBytes);
+        if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], bytes);
         const uint32_t bar = leader_addr<2>(&sm.full[stage]);
         uint8_t* da = sm.base + stage * C::kStageBytes;
         uint8_t* db = da + C::kTile;
@@ -256,7 +265,7 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
         }
         if (BMN) {
           tma_load_2d<2>(db, mb, b0, k, bar);
-          tma_load_2d<2>(db + 8192, mb, b0 + 64, k, bar);
+          if (s.bn == 256) tma_load_2d<2>(db + 8192, mb, b0 + 64, k, bar);
         } else {
           tma_load_2d<2>(db, mb, k, b0, bar);
         }
@@ -342,15 +351,15 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
   for (int32_t u = cluster_id; u < s.units; u += clusters, ++st.it) {
     const OrthoUnit t = ortho_unit<SYM>(s, u);
     const uint32_t acc = st.it & 1;
-    const int32_t row0 = t.tm * 256 + 128 * (int32_t)rank + sp * 32, row = row0 + lane;
+    const int32_t row0 = t.y0 + 128 * (int32_t)rank + sp * 32, row = row0 + lane;
     const int32_t chunks = t.cols >> 5;
     const int32_t c0 = t.part + t.parts * half, dc = 2 * t.parts;  // this warp's chunks
     const bool rows_in = row0 < s.rows_a;
-    const bool mirror = SYM && t.tn < t.tm;
+    const bool mirror = SYM && t.x0 < t.y0;
     // brings the epilogue's inputs of a chunk into a buffer
     auto prefetch = [&](int32_t c, uint32_t b) {
       uint8_t* buf = bufs + b * C::kBuf;
-      const int32_t x = t.tn * 256 + c * 32;
+      const int32_t x = t.x0 + c * 32;
       mbar_arrive_expect_tx(&src_bar[b], EPI == kOrthoUpdate ? 4096 : 2048);
       tma_load_2d<1>(buf, src_hi, x, row0, smem_u32(&src_bar[b]));
       if (EPI == kOrthoUpdate) tma_load_2d<1>(buf + 2048, src_lo, x, row0, smem_u32(&src_bar[b]));
@@ -367,7 +376,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
     if (row < s.rows_a && (EPI == kOrthoPoly || (EPI == kOrthoUpdate && !TALL))) dr = __ldcg(diag + row);
     // the diagonal at a chunk's columns, one per lane
     auto load_diag = [&](int32_t c) {
-      const int32_t x = t.tn * 256 + c * 32 + lane;
+      const int32_t x = t.x0 + c * 32 + lane;
       return kCols && c < chunks && x < s.rows_b ? __ldcg(diag + x) : 0.f;
     };
     float d_next = load_diag(c0);
@@ -411,7 +420,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
       uint8_t* buf_l = buf_h + 2048;
       uint8_t* my_h = buf_h + lane * 64;
       uint8_t* my_l = buf_l + lane * 64;
-      const int32_t col0 = t.tn * 256 + c * 32;
+      const int32_t col0 = t.x0 + c * 32;
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_base + c * 32, r);
       const float dc_lane = d_next;
@@ -634,10 +643,11 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
       const int type = i % 3, cur = (i / 3) & 1;
       bool ok;
       if (type == kOrthoGram)
-        ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram[cur][0],
-                                          &m.gram[cur][1], cluster_id, clusters, rank, stage, phase, issued, issued_phase);
+        ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram_b[cur][0],
+                                          &m.gram_b[cur][1], cluster_id, clusters, rank, stage, phase, issued,
+                                          issued_phase);
       else if (type == kOrthoPoly)
-        ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o, &m.o, cluster_id, clusters, rank,
+        ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o_b, &m.o_b, cluster_id, clusters, rank,
                                             stage, phase, issued, issued_phase);
       else if (TALL)
         ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,

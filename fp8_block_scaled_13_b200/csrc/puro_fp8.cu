@@ -1223,11 +1223,17 @@ constexpr int kOrthoMaxSteps = 64;
 constexpr int64_t kOrthoMaxDim = 65536;
 
 // How the three products of a step are cut into units for 74 CTA pairs (see
-// ortho.cuh).  The tiles beyond the last full round of pairs are split along k
-// where that spares a pair at least kOrthoSpare of its 64-deep blocks; handing
-// the partials over costs about as much as six of them.
+// ortho.cuh): the tile width, and for the tiles beyond the last full round of
+// pairs a split along k, that together should take the least time.  In cycles,
+// measured on a B200: a 64-deep block of a tile, by its width; 32 columns of an
+// epilogue, which two sets of warps share; a split tile's hand-over, and writing
+// and reading 32 columns of partials.  (200 x 333: 125 us against 166 with 256
+// columns throughout, 512 x 512: 133 against 180, 2048 x 2048: 253 against 268,
+// and 402 with 64 throughout.)
 constexpr int64_t kOrthoPairs = kSms / 2;
-constexpr int64_t kOrthoSpare = 10;
+constexpr int64_t kOrthoBlockCycles[3] = {530, 430, 340};  // 256, 128, 64 columns
+constexpr int64_t kOrthoChunkCycles = 2200;
+constexpr int64_t kOrthoSplitCycles = 3000, kOrthoWriteCycles = 300, kOrthoReadCycles = 350;
 constexpr int64_t kOrthoLeast = 4;  // blocks that a part keeps
 static_assert(kOrthoPairs <= puro::kSplitTiles, "counters for every split tile");
 
@@ -1247,22 +1253,37 @@ OrthoPlan ortho_plan(int64_t n, int64_t k) {
     s.rows_b = (int32_t)cols[i];
     s.kblocks = (int32_t)((sums[i] + 63) / 64);
     s.passes = i == puro::kOrthoGram && w <= puro::kOrthoExactK ? 3 : 1;
-    const int64_t tm = (rows[i] + 255) / 256, tn = (cols[i] + 255) / 256, total = (int64_t)s.kblocks * s.passes;
-    const int64_t tiles = i == puro::kOrthoUpdate ? tm * tn : tm * (tm + 1) / 2;
-    const int64_t rest = tiles % kOrthoPairs;
-    s.tiles_m = (int32_t)tm;
-    s.tiles_n = (int32_t)tn;
-    s.split = 1;
-    s.full = s.units = (int32_t)tiles;
-    if (rest) {
-      int64_t split = std::min<int64_t>({kOrthoPairs / rest, puro::kOrthoMaxSplit, total / kOrthoLeast});
-      if (split > 1 && total - (total + split - 1) / split >= kOrthoSpare) {
+    const int64_t tm = (rows[i] + 255) / 256, total = (int64_t)s.kblocks * s.passes;
+    int64_t best = INT64_MAX;
+    for (int j = 0; j < 3; ++j) {
+      const int64_t bn = 256 >> j, tn = (cols[i] + bn - 1) / bn, block = kOrthoBlockCycles[j];
+      int64_t tiles = tm * tn;
+      if (i != puro::kOrthoUpdate) {
+        tiles = 0;
+        for (int64_t t = 0; t < tm; ++t) tiles += std::min(tn, (t + 1) * (256 / bn));
+      }
+      const int64_t chunks = std::min(bn, (cols[i] + 31) / 32 * 32) / 32;
+      for (int64_t split = 1; split <= puro::kOrthoMaxSplit; ++split) {
+        const int64_t rest = tiles % kOrthoPairs;
+        if (split > 1 && (rest == 0 || rest * split > kOrthoPairs || total / split < kOrthoLeast)) break;
+        const int64_t rounds = split > 1 ? tiles / kOrthoPairs : (tiles + kOrthoPairs - 1) / kOrthoPairs;
+        int64_t cost = rounds * total * block;
+        const int64_t own = (chunks + split - 1) / split;  // chunks that a part of the last tile finishes
+        if (split > 1)
+          cost += (total + split - 1) / split * block + kOrthoSplitCycles + (chunks - own) * kOrthoWriteCycles +
+                  own * (split - 1) * kOrthoReadCycles;
+        cost += (own + 1) / 2 * kOrthoChunkCycles;
+        if (cost >= best) continue;
+        best = cost;
+        s.bn = (int32_t)bn;
+        s.tiles_m = (int32_t)tm;
+        s.tiles_n = (int32_t)tn;
         s.split = (int32_t)split;
-        s.full = (int32_t)(tiles - rest);
-        s.units = (int32_t)(s.full + rest * split);
-        plan.split_units = std::max(plan.split_units, rest * split);
+        s.full = (int32_t)(split > 1 ? tiles - rest : tiles);
+        s.units = (int32_t)(split > 1 ? s.full + rest * split : tiles);
       }
     }
+    if (s.split > 1) plan.split_units = std::max<int64_t>(plan.split_units, s.units - s.full);
     plan.pairs = std::max(plan.pairs, std::min<int64_t>(s.units, kOrthoPairs));
   }
   return plan;
@@ -1408,16 +1429,19 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
   // (MN-major), and everything as the epilogue reads and writes it
   puro::OrthoMaps maps;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_e = CU_TENSOR_MAP_SWIZZLE_64B;
+  auto half = [&](int product) { return (uint32_t)plan.shape[product].bn / 2; };
   for (int i = 0; i < 2; ++i) {
     for (int t = 0; t < 2; ++t) {
       if ((st = make_map_16(&maps.gram[i][t], at(l.x[i][t]), k, n, l.ld_x, 64, tall ? 64 : 128, sw)) != PURO_OK ||
+          (st = make_map_16(&maps.gram_b[i][t], at(l.x[i][t]), k, n, l.ld_x, 64, tall ? 64 : half(0), sw)) != PURO_OK ||
           (st = make_map_16(&maps.ex[i][t], at(l.x[i][t]), k, n, l.ld_x, 32, 32, sw_e)) != PURO_OK)
         return st;
     }
     if ((st = make_map_16(&maps.update[i], at(l.x[i][0]), k, n, l.ld_x, 64, tall ? 128 : 64, sw)) != PURO_OK) return st;
   }
   if ((st = make_map_16(&maps.o, at(l.o), m, m, l.ld_m, 64, 128, sw)) != PURO_OK ||
-      (st = make_map_16(&maps.r, at(l.r), m, m, l.ld_m, 64, 128, sw)) != PURO_OK ||
+      (st = make_map_16(&maps.o_b, at(l.o), m, m, l.ld_m, 64, half(1), sw)) != PURO_OK ||
+      (st = make_map_16(&maps.r, at(l.r), m, m, l.ld_m, 64, tall ? half(2) : 128, sw)) != PURO_OK ||
       (st = make_map_16(&maps.eo, at(l.o), m, m, l.ld_m, 32, 32, sw_e)) != PURO_OK ||
       (st = make_map_16(&maps.er, at(l.r), m, m, l.ld_m, 32, 32, sw_e)) != PURO_OK)
     return st;
