@@ -212,7 +212,7 @@ __host__ __device__ constexpr uint32_t norm_pass_smem(int rows, int32_t threads,
 // The forward row pass: y, the norms' factors and, if asked for, n as row-wise
 // codes or BF16.
 template <int MAXT, int B>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_forward_kernel(const NormParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1) norm_forward_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t nsmem[];
   float* red = reinterpret_cast<float*>(nsmem);
   const uint8_t* ring = nsmem + kNormRedBytes;

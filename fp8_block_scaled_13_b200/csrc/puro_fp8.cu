@@ -947,7 +947,7 @@ int launch_norm_forward(puro::NormParams p, const DeviceInfo& dev, cudaStream_t 
   static std::atomic<bool> done[kMaxDevices] = {};
   // 16 forward, for an even end (32768 x 2048: 119 us; 125 with 32 rows, 124 with
   // 8), but 32 where one CTA fills an SM (8192 x 8192: 138 us against 141)
-  p.rpc = norm_rpc(p.rows, MAXT == 256 ? 3 : 1, MAXT == 1024 ? 32 : 16, 1);
+  p.rpc = norm_rpc(p.rows, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1, MAXT == 1024 ? 32 : 16, ROWS);
   const int threads = (p.cols / 8 + 31) / 32 * 32;
   const int tensors = 1 + (p.h != nullptr) + (p.gate_kind == PURO_GATE_FULL);
   return launch_norm_pass(puro::norm_forward_kernel<MAXT, ROWS>, done, puro::norm_pass_smem(ROWS, MAXT, 3), p,
@@ -1081,7 +1081,7 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
   p.rstd_post = rstd_post;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   r = cols <= 2048   ? launch_norm_forward<256, 4>(p, *dev, sm)
-      : cols <= 4096 ? launch_norm_forward<512, 4>(p, *dev, sm)
+      : cols <= 4096 ? launch_norm_forward<512, 2>(p, *dev, sm)
                      : launch_norm_forward<1024, 2>(p, *dev, sm);
   if (r != PURO_OK || !col) return r;
   puro::QuantParams qp = quant_params(out, rows, cols, p.ctr);

@@ -76,18 +76,24 @@ def _on_operand_device(fn):
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         operands = (*args, *kwargs.values()) if kwargs else args
-        dev = None
+        dev, same = None, True
         for a in operands:
             kind = type(a)
-            if kind in _PLAIN:
-                continue
-            for t in (a,) if kind is torch.Tensor else _tensors(a):
+            if kind is torch.Tensor:
                 if dev is None:
-                    dev = t.device
-                elif t.device != dev:
-                    devs = {t.device for a in operands for t in _tensors(a)}
-                    raise ValueError("%s: operands are on different devices (%s)"
-                                     % (fn.__name__, ", ".join(sorted(str(d) for d in devs))))
+                    dev = a.device
+                elif a.device != dev:
+                    same = False
+            elif kind not in _PLAIN:
+                for t in _tensors(a):
+                    if dev is None:
+                        dev = t.device
+                    elif t.device != dev:
+                        same = False
+        if not same:
+            devs = {t.device for a in operands for t in _tensors(a)}
+            raise ValueError("%s: operands are on different devices (%s)"
+                             % (fn.__name__, ", ".join(sorted(str(d) for d in devs))))
         if dev is not None and dev.type == "cuda" and dev.index != _current_device():
             with torch.cuda.device(dev):
                 return fn(*args, **kwargs)
