@@ -1,9 +1,11 @@
-"""Build the CUDA library libpuro_fp8.so in-tree (nvcc, sm_100a only)."""
+"""Build the CUDA library libpuro_fp8.so (nvcc, sm_100a only) and the compiled
+wrappers _binding.so (g++, against torch) in-tree."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -13,6 +15,8 @@ SOURCES = ["puro_fp8.cu"]
 DEPS = ["puro_fp8.cu", "common.cuh", "quant.cuh", "gemm.cuh", "norm.cuh", "gated.cuh",
         "ortho.cuh"]
 HEADER = os.path.join(ROOT, "include", "puro_fp8.h")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 
 def nvcc_path() -> str:
@@ -37,12 +41,24 @@ def nvcc_command(out: str, verbose_ptxas: bool = False) -> list:
     return cmd
 
 
+def binding_command(out: str) -> list:
+    import torch
+
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-o", out, BINDING_SOURCE,
+            *("-I" + d for d in include), "-L" + HERE, "-l:" + os.path.basename(LIB_PATH),
+            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+
+
+def _stale(out: str, deps: list) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(d) > os.path.getmtime(out) for d in deps)
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, d) for d in DEPS] + [HEADER]
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _stale(LIB_PATH, [os.path.join(CSRC, d) for d in DEPS] + [HEADER])
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -50,6 +66,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
         subprocess.run(nvcc_command(tmp, verbose_ptxas), check=True)
         os.replace(tmp, LIB_PATH)
+    if force or _stale(BINDING_PATH, [BINDING_SOURCE, HEADER]):
+        tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+        subprocess.run(binding_command(tmp), check=True)
+        os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
 
