@@ -34,13 +34,17 @@ def _row_stride(t: torch.Tensor) -> int:
 @_on_operand_device
 def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """The nearly orthogonal matrix of g [n, k] (FP32 or BF16) that `steps` Newton-Schulz steps with the odd quintic
-    a x + b x^3 + c x^5 reach from g / (|g| + eps), as BF16 [n, k].
+    """The nearly orthogonal matrix of g [n, k] (FP32 or BF16, n, k <= 65536) that `steps` Newton-Schulz steps with the
+    odd quintic a x + b x^3 + c x^5 reach from g / (|g| + eps), as BF16 [n, k].
 
+    The coefficients must keep singular values that start in [0, 1] below 2, as Muon's do.  |g| is summed in FP32: it
+    has to stay below 1e18, and eps should be small beside it (a g / eps below 1e-4 loses digits).
     `workspace`: a contiguous CUDA uint8 tensor of puro_fp8_orthogonalize_workspace_bytes(n, k) bytes to use instead
     of allocating it; calls that may run at the same time need distinct ones."""
     _matrix(g, (torch.float32, torch.bfloat16), "g")
     n, k = g.shape
+    if n > 65536 or k > 65536:
+        raise ValueError("g must be at most [65536, 65536], got [%d, %d]" % (n, k))
     if not 1 <= steps <= 64:
         raise ValueError("steps must be 1 to 64, got %r" % (steps,))
     if not eps >= 0:
@@ -62,5 +66,7 @@ def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7
         raise ValueError("workspace must be a contiguous CUDA uint8 tensor of at least %d bytes" % need)
     st = _lib.puro_fp8_orthogonalize(g.data_ptr(), _row_stride(g), int(g.dtype == torch.float32), n, k, steps, a, b, c,
                                      eps, out.data_ptr(), _row_stride(out), workspace.data_ptr(), _stream())
+    if st == _lib.PURO_ERR_SHAPE:
+        raise ValueError("the coefficients %r lead singular values out of range in %d steps" % (coefficients, steps))
     _check(st, "puro_fp8_orthogonalize")
     return out

@@ -394,9 +394,13 @@ PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
  *        stride ld_g >= k and any alignment of its type; |g| below 1e18 (its
  *        squares are summed in FP32).
  * out  : BF16 [n, k], any row stride ld_out >= k; must not overlap g.
- * Every matrix between is held to 16 significant bits (two BF16 terms), every
- * product accumulates in FP32, and out is rounded to BF16 once.
- * 1 <= n, k <= 65536 (0: no-op); 1 <= steps <= 64; eps >= 0.
+ * X is held to 22 significant bits (two FP16 terms), the diagonals of M and of
+ * b M + c M^2 in FP32, and every product accumulates in FP32; what enters a
+ * product is rounded to FP16 off the diagonal, and out to BF16 once.
+ * 1 <= n, k <= 65536 (0: no-op); 1 <= steps <= 64; eps >= 0; coefficients that
+ * let a singular value from [0, 1] reach 2 are refused (PURO_ERR_SHAPE).
+ * The products run as one cooperative launch, which waits until all its CTAs
+ * fit on the device beside what else runs there.
  */
 PURO_API int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, int64_t n, int64_t k,
                                     int steps, float a, float b, float c, float eps, void* out,

@@ -316,3 +316,67 @@ def test_repeatable(fp8):
         r = fp8.residual_norm_backward(dn, f.y, f.rstd, w, h, w_post=w, rstd_post=f.rstd_post)
         assert torch.equal(r.dw_pre, one.dw_pre) and torch.equal(r.dw_post, one.dw_post)
         assert torch.equal(r.dh.q, one.dh.q) and torch.equal(r.dh.qt, one.dh.qt)
+
+
+def test_wrapper_refusals(fp8):
+    """Whatever does not fit is refused before any launch, with the name of the argument."""
+    t, d = 16, 256
+    x, h, w = _bf((t, d), 1), _bf((t, d), 2), torch.ones(d, device="cuda")
+    f = fp8.residual_norm(x, w, h, w_post=w)
+    n = lambda *a, **k: lambda: fp8.residual_norm(*a, **k)  # noqa: E731
+    b = lambda *a, **k: lambda: fp8.residual_norm_backward(*a, **k)  # noqa: E731
+    args = (x, f.y, f.rstd, w, h)
+    other = fp8.residual_norm(_bf((t, 128), 1), w[:128]).n
+    rowwise = fp8.residual_norm(x, w, layout="rowwise").n
+    for match, call in [
+            ("layout", n(x, w, layout="columns")), ("eps", n(x, w, eps=0.0)), ("x must", n(x.float(), w)),
+            ("x must", n(x.T, w)), ("x must", n(x[0], w)), ("w_pre must", n(x, w[:-1])), ("w_pre must", n(x, w.half())),
+            ("w_pre must", n(x, torch.ones(2 * d, device="cuda")[::2])), ("one type", n(x, w, h, w_post=w.bfloat16())),
+            ("h must", n(x, w, h[:-1])), ("missing", n(x, w, gate=w[None])), ("missing", n(x, w, w_post=w)),
+            ("only written", n(x, w, y=x)), ("y must", n(x, w, h, y=x.float())), ("gate must", n(x, w, h, gate=w)),
+            ("gate must", n(x, w, h, gate=w[None].half())), ("per element", n(x, w, h, gate=x.float())),
+            ("per token", n(x, w, h, gate=torch.ones(2 * t, 1, device="cuda")[::2])),
+            ("QuantAct", n(x, w, out=other)), ("QuantAct", n(x, w, out=x)), ("transposed codes", n(x, w, out=rowwise)),
+            ("BF16 tensor", n(x, w, layout="bf16", out=rowwise)), ("out must", n(x, w, layout="bf16", out=x[:-1])),
+            ("CUDA", n(x.cpu(), w.cpu())), ("different devices", n(x, w.cpu())),
+            ("y must", b(x, f.y[:-1], f.rstd, w)), ("rstd must", b(x, f.y, f.rstd[:-1], w)),
+            ("rstd_post", b(*args, w_post=w)), ("rstd_post must", b(*args, w_post=w, rstd_post=f.rstd_post.double())),
+            ("missing", b(x, f.y, f.rstd, w, out=rowwise)), ("need w_post", b(*args, dw_post=w)),
+            ("need w_post", b(*args, dgate=w)), ("accumulate", b(*args, accumulate=True)),
+            ("accumulate", b(*args, gate=w[None], dw_pre=w, accumulate=True)), ("dw_pre must", b(*args, dw_pre=w[:-1])),
+            ("dgate must", b(*args, gate=w[None], dgate=w)), ("dx must", b(*args, dx=w)), ("dy must", b(*args, dy=x[:-1])),
+            ("two halves", lambda: fp8.swiglu(torch.zeros(4, 257, dtype=torch.bfloat16, device="cuda"))),
+            ("gu must", lambda: fp8.swiglu_backward(x, x))]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    for wrong in (None, 3, "x"):
+        with pytest.raises(TypeError, match="tensor"):
+            fp8.swiglu(wrong)
+    with pytest.raises(fp8_error(fp8)):   # a width that the library does not take
+        fp8.residual_norm(_bf((4, 200), 1), torch.ones(200, device="cuda"), layout="bf16")
+    assert fp8.device_status() == 0
+
+
+def fp8_error(fp8):
+    from fp8_block_scaled_13_b200._lib import PuroError
+    return PuroError
+
+
+def test_on_another_stream_than_the_tensors(fp8):
+    """Calls go to the current stream; memory that a side stream still writes is waited for by that stream's order."""
+    t, d = 4096, 2048
+    w = 1 + 0.1 * torch.randn(d, device="cuda")
+    src, da = _bf((t, 2 * d), 1), _bf((t, d), 2)
+    want = [fp8.swiglu(src).q.clone(), fp8.residual_norm(src[:, :d].contiguous(), w).n.qt.clone(),
+            fp8.swiglu_backward(da, src).qt.clone()]
+    side = torch.cuda.Stream()
+    x = torch.zeros_like(src)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            x.mul_(0.5)     # work in front of the copy
+        x.copy_(src)
+        got = [fp8.swiglu(x).q, fp8.residual_norm(x[:, :d].contiguous(), w).n.qt, fp8.swiglu_backward(da, x).qt]
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

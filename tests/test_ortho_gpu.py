@@ -157,3 +157,26 @@ def test_streams_workspaces_and_graphs(fp8):
         for i in range(2):
             assert torch.equal(out[i], want[i] * flip)
     assert fp8.device_status() == 0
+
+
+def test_refusals(fp8):
+    g = _gradient(64, 96, 1, torch.float32)
+    ws = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    bad = [dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(coefficients=(4.0, 0.0, 0.0)),
+           dict(coefficients=(float("nan"), 0.0, 0.0)), dict(out=torch.empty(64, 95, dtype=torch.bfloat16, device="cuda")),
+           dict(out=torch.empty(64, 96, device="cuda")), dict(out=torch.empty(64, 96, dtype=torch.bfloat16)),
+           dict(out=torch.empty(96, 64, dtype=torch.bfloat16, device="cuda").T), dict(workspace=ws),
+           dict(workspace=ws.cpu()), dict(workspace=ws.float())]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            fp8.orthogonalize(g, **kw)
+    half = g.to(torch.bfloat16)
+    for wrong in (g.half(), g.double(), g.T, g[0], g.reshape(2, 32, 96)):
+        with pytest.raises(ValueError):
+            fp8.orthogonalize(wrong)
+    with pytest.raises(ValueError, match="overlap"):
+        fp8.orthogonalize(half, out=half)
+    wide = torch.empty(2, 65537, device="cuda")
+    with pytest.raises(ValueError, match="65536"):
+        fp8.orthogonalize(wide)
+    assert fp8.device_status() == 0
