@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libpuro_fp8.so")
 SOURCES = ["puro_fp8.cu"]
 DEPS = ["puro_fp8.cu", "common.cuh", "quant.cuh", "gemm.cuh", "norm.cuh", "gated.cuh",
-        "ortho.cuh"]
+        "ortho.cuh", "ortho_small.cuh"]
 HEADER = os.path.join(ROOT, "include", "puro_fp8.h")
 BINDING_PATH = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")

@@ -161,7 +161,7 @@ def test_streams_workspaces_and_graphs(fp8):
 
 def test_refusals(fp8):
     g = _gradient(64, 96, 1, torch.float32)
-    ws = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(255, dtype=torch.uint8, device="cuda")  # the smallest workspace is 256 bytes
     bad = [dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(coefficients=(4.0, 0.0, 0.0)),
            dict(coefficients=(float("nan"), 0.0, 0.0)), dict(out=torch.empty(64, 95, dtype=torch.bfloat16, device="cuda")),
            dict(out=torch.empty(64, 96, device="cuda")), dict(out=torch.empty(64, 96, dtype=torch.bfloat16)),
