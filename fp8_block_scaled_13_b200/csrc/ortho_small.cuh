@@ -47,8 +47,8 @@ struct OrthoSmallCfg {
   static constexpr uint32_t kTile = 128 * 128;              // [128][64] FP16, 128-byte swizzle
   static constexpr uint32_t kOffLo = 2 * kTile;             // X hi: two tiles, X lo: two
   static constexpr uint32_t kOffO = 4 * kTile;              // O, then R
-  static constexpr uint32_t kOffSum = 6 * kTile;            // partial M: [32 column quads][128 rows] float4
-  static constexpr uint32_t kOffDiag = kOffSum + 65536;     // D, D'
+  static constexpr uint32_t kOffSum = 6 * kTile;            // partial M, two buffers: [32 column quads][128 rows] float4
+  static constexpr uint32_t kOffDiag = kOffSum + 2 * 65536; // D, D'
   static constexpr uint32_t kOffRed = kOffDiag + 1024;      // sums of squares: 8 warps, the CTA's
   static constexpr uint32_t kOffMisc = kOffRed + 64;        // barrier, TMEM address, abort flag
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
@@ -269,20 +269,45 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     }
     finish();
     // ---- O and D
+    float4* mine = sums + (step & 1) * 4096;  // (alternating, so that no barrier has to follow the reads)
+    if (peers > 1) {
 #pragma unroll 1
-    for (int c = col0; c < col0 + 64 && c < m16; c += 32) {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tmem + t_row + c, r);
-      tmem_ld_wait();
-      regs_after_wait(r);
-      float v[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * (kMScale / (kXScale * kXScale));
-      if (peers > 1) {
+      for (int c = col0; c < col0 + 64 && c < m16; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + t_row + c, r);
+        tmem_ld_wait();
+        regs_after_wait(r);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          sums[(c / 4 + q) * 128 + row] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-      } else {
+          mine[(c / 4 + q) * 128 + row] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                                      __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+      }
+      cluster_or_block_sync<2>();
+    }
+    constexpr float kToM = kMScale / (kXScale * kXScale);
+    if (peers <= 2) {
+#pragma unroll 1
+      for (int c = col0; c < col0 + 64 && c < m16; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + t_row + c, r);
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        if (peers == 2) {
+          const uint32_t from = cluster_peer(smem_u32(mine + (c / 4) * 128 + row), rank ^ 1);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = ld_peer_f4(from + q * 2048);
+            v[4 * q] = f.x;
+            v[4 * q + 1] = f.y;
+            v[4 * q + 2] = f.z;
+            v[4 * q + 3] = f.w;
+          }
+        }
+        tmem_ld_wait();
+        regs_after_wait(r);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = (__uint_as_float(r[e]) + v[e]) * kToM;
         if ((row & ~31) == c) {
           float d = 0.f;
 #pragma unroll
@@ -299,9 +324,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
               make_uint4(half_pair(v[8 * q], v[8 * q + 1]), half_pair(v[8 * q + 2], v[8 * q + 3]),
                          half_pair(v[8 * q + 4], v[8 * q + 5]), half_pair(v[8 * q + 6], v[8 * q + 7]));
       }
-    }
-    if (peers > 1) {
-      cluster_or_block_sync<2>();
+      hand_over();
+    } else {
       // the band of rows that this CTA adds, 8 columns at a time
       const int band = 128 / (int)peers, first = (int)rank * band;
       for (int i = tid; i < band * (m16 / 8); i += kSmallThreads) {
@@ -309,19 +333,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        const uint32_t at = smem_u32(sums + (c / 4) * 128 + r);
-        for (uint32_t q = 0; q < peers; ++q) {
-          const uint32_t from = cluster_peer(at, q);
-          const float4 f = ld_peer_f4(from), g = ld_peer_f4(from + 128 * 16);
-          v[0] += f.x;
-          v[1] += f.y;
-          v[2] += f.z;
-          v[3] += f.w;
-          v[4] += g.x;
-          v[5] += g.y;
-          v[6] += g.z;
-          v[7] += g.w;
+        const uint32_t at = smem_u32(mine + (c / 4) * 128 + r);
+        for (uint32_t q = 0; q < peers; q += 4) {  // (four or more: eight loads in flight)
+          float4 f[4], g[4];
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t from = cluster_peer(at, q + k);
+            f[k] = ld_peer_f4(from);
+            g[k] = ld_peer_f4(from + 128 * 16);
+          }
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) {
+            v[0] += f[k].x;
+            v[1] += f[k].y;
+            v[2] += f[k].z;
+            v[3] += f[k].w;
+            v[4] += g[k].x;
+            v[5] += g[k].y;
+            v[6] += g[k].z;
+            v[7] += g[k].w;
+          }
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= kToM;
         float d = 0.f;
         const bool on_diag = (r & ~7) == c;
         if (on_diag) {
@@ -344,8 +378,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
       cluster_or_block_sync<2>();
       tc_fence_after();
       fence_proxy_async_all();
-    } else {
-      hand_over();
     }
     // ---- S = O O
     if (warp == 0) {
