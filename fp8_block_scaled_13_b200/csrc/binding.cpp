@@ -1,11 +1,11 @@
-// The argument handling of the block operators' Python wrappers (block.py): the
+// The argument handling of the Python wrappers in block.py and muon.py: the
 // checks, the allocation of outputs and the call into libpuro_fp8.so.  These
 // operators run for a few microseconds on small inputs and take up to 20
 // tensors; checking those in Python took two to three times as long as the GPU
 // needed (the norm of 16 rows: 13 us of 20; its backward pass: 30 of 43).
 // Everything is refused here as the Python wrappers of the linear layers refuse
 // it: ValueError before any launch; a status of the library is returned as the
-// first value and raised by block.py.
+// first value and raised there.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <exception>
 #include <initializer_list>
@@ -510,8 +511,60 @@ PyObject* swiglu_backward(PyObject* const* a, Py_ssize_t n) {
   return results(st, {&res.nq, &res.ns, &res.nqt, &res.nst, &res.nbf});
 }
 
+// A row-major matrix of any row stride, also a view into a wider one: its row stride.
+int64_t need_rows(const Arg& a) {
+  const at::Tensor& t = *a.t;
+  if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) < t.size(1)))
+    value_error("%s must be a row-major 2-D tensor", a.name);
+  return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1));
+}
+
+// g, steps, a, b, c, eps, out, workspace -> status, out
+PyObject* orthogonalize(PyObject* const* a, Py_ssize_t n_args) {
+  need_count(n_args, 8);
+  const Arg g(a[0], "g", false), out(a[6], "out"), workspace(a[7], "workspace");
+  const int steps = integer(a[1]);
+  const float ca = (float)number(a[2]), cb = (float)number(a[3]), cc = (float)number(a[4]), eps = (float)number(a[5]);
+  const OnDevice dev("orthogonalize", {&g, &out, &workspace});
+  need_cuda(g);
+  const at::ScalarType type = g.t->scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16)
+    value_error("g must be torch.float32 or torch.bfloat16, got %s", type_name(type).c_str());
+  const int64_t ld_g = need_rows(g), n = g.t->size(0), k = g.t->size(1);
+  if (n > 65536 || k > 65536)
+    value_error("g must be at most [65536, 65536], got [%lld, %lld]", (long long)n, (long long)k);
+  if (steps < 1 || steps > 64) value_error("steps must be 1 to 64, got %d", steps);
+  if (!(eps >= 0)) value_error("eps must not be negative");
+  at::Tensor result;
+  int64_t ld_out = k;
+  if (out) {
+    need_type(out, at::kBFloat16);
+    ld_out = need_rows(out);
+    if (out.t->size(0) != n || out.t->size(1) != k)
+      value_error("out must be [%lld, %lld], got %s", (long long)n, (long long)k, shape_name(*out.t).c_str());
+    const char *g0 = static_cast<const char*>(g.ptr()), *o0 = static_cast<const char*>(out.ptr());
+    if (n && k && g0 < o0 + ((n - 1) * ld_out + k) * 2 && o0 < g0 + ((n - 1) * ld_g + k) * (type == at::kFloat ? 4 : 2))
+      value_error("out must not overlap g");
+  } else {
+    result = dev.empty({n, k}, at::kBFloat16);
+  }
+  const int64_t need = puro_fp8_orthogonalize_workspace_bytes(n, k);
+  at::Tensor ws;
+  if (workspace)
+    need_bytes(workspace, need);
+  else
+    ws = dev.empty({need > 256 ? need : 256}, at::kByte);
+  void* stream = dev.stream();
+  const int st = unlocked([&] {
+    return puro_fp8_orthogonalize(g.ptr(), ld_g, type == at::kFloat, n, k, steps, ca, cb, cc, eps,
+                                  Result::at_(out, result), ld_out, Result::at_(workspace, ws), stream);
+  });
+  return results(st, {&result});
+}
+
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(residual_norm), ENTRY(residual_norm_backward), ENTRY(swiglu), ENTRY(swiglu_backward),
+                         ENTRY(orthogonalize),
                          {nullptr, nullptr, 0, nullptr}};
 #undef ENTRY
 
