@@ -12,11 +12,11 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <cstdarg>
-#include <exception>
 #include <initializer_list>
 #include <set>
 #include <string>
@@ -353,20 +353,17 @@ int unlocked(F f) {
   return st;
 }
 
-// Turns C++ exceptions into Python ones.
+// Turns C++ exceptions into Python ones, torch's (out of memory among them) into
+// what torch makes of them.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   try {
     return F(args, n);
   } catch (const PythonError&) {
     return nullptr;
-  } catch (const c10::Error& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-    return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
   }
+  END_HANDLE_TH_ERRORS
 }
 
 // x, w_pre, h, w_post, gate, scale, eps, layout, y, out

@@ -76,6 +76,23 @@ def test_any_strides_and_alignment(fp8, n, k):
             assert (out[:, :shift] == -7).all() and (out[:, shift + k:] == -7).all()
 
 
+# the kernel of one cluster: every size of cluster, an empty slice, slices and sides that end inside a tile
+@pytest.mark.parametrize("n,k", [(128, 129), (129, 128), (3, 257), (128, 384), (511, 77), (100, 1025), (1, 2048), (2048, 128),
+                                 (17, 1999), (2047, 33), (127, 1153)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small_sides(fp8, n, k, dtype):
+    g = _gradient(n, k, n + 2 * k, dtype)
+    got = fp8.orthogonalize(g)
+    assert _error(got, _reference(g)) <= BOUND
+    assert torch.equal(fp8.orthogonalize(g), got)
+    wide = torch.full((n, k + 9), float("nan"), dtype=dtype, device="cuda")
+    wide[:, 1:k + 1] = g
+    out = torch.full((n, k + 11), 5.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(fp8.orthogonalize(wide[:, 1:k + 1], out=out[:, 3:k + 3]), got)
+    assert (out[:, :3] == 5).all() and (out[:, k + 3:] == 5).all()
+    assert fp8.device_status() == 0
+
+
 # every way a product is cut: one tile; rounds of whole tiles; the rest split; three products or one for X X^T
 @pytest.mark.parametrize("n,k", [(256, 256), (512, 2048), (1536, 1536), (2048, 1024), (2560, 2048), (300, 5000), (5000, 300),
                                  (4100, 2050)])
@@ -126,9 +143,10 @@ def test_size_of_the_gradient(fp8):
         assert fp8.orthogonalize(torch.empty(shape, device="cuda")).shape == shape
 
 
-def test_streams_workspaces_and_graphs(fp8):
+@pytest.mark.parametrize("n,k", [(600, 1100), (8, 2000), (150, 200)])
+def test_streams_workspaces_and_graphs(fp8, n, k):
     from fp8_block_scaled_13_b200 import _lib
-    gs = [_gradient(600 + 40 * i, 1100, i, torch.float32) for i in range(4)]
+    gs = [_gradient(n + 40 * i, k, i, torch.float32) for i in range(4)]
     want = [fp8.orthogonalize(g) for g in gs]
     streams = [torch.cuda.Stream() for _ in gs]
     torch.cuda.synchronize()
