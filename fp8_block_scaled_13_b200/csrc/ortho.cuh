@@ -90,6 +90,7 @@ struct OrthoParams {
   __nv_bfloat16* out;       // the BF16 result, by plain stores if out_tma is 0
   int64_t ld_out;
   int32_t out_tma;
+  int32_t one_cluster;      // the grid is one cluster, whose barrier separates the products
 };
 constexpr int kPartial = 2 * 8 * 4 * 8 * 32;  // float4 of a tile's partials: [CTA][chunk][32 rows][8][lane]
 constexpr int kSplitTiles = 74;  // most tiles that can be split: fewer than CTA pairs
@@ -232,7 +233,27 @@ struct OrthoSmem {
   uint8_t* base;
   uint64_t *full, *empty, *accf, *acce, *drain, *ready, *done, *parts_out, *parts_in, *src;
   volatile int* abort_flag;
+  uint32_t pair;  // rank of the pair's first CTA, the leader, in the cluster
 };
+
+// `p` in the pair's leader.
+__device__ __forceinline__ uint32_t pair_leader(const OrthoSmem& sm, const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(sm.pair));
+  return a;
+}
+
+// Arrive on `bar` in both CTAs of the pair when the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(const OrthoSmem& sm, uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)(3u << sm.pair))
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The producer warp's share of one product.
 template <bool SYM, bool AMN, bool BMN>
@@ -252,7 +273,7 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
       if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1, sm.abort_flag)) return false;
       if (elect_one()) {
         if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], bytes);
-        const uint32_t bar = leader_addr<2>(&sm.full[stage]);
+        const uint32_t bar = pair_leader(sm, &sm.full[stage]);
         uint8_t* da = sm.base + stage * C::kStageBytes;
         uint8_t* db = da + C::kTile;
         const CUtensorMap* ma = pass == 2 ? al : ah;
@@ -308,14 +329,14 @@ __device__ __forceinline__ bool ortho_mma(const OrthoSmem& sm, const OrthoShape&
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           tc_mma_f16(tmem + acc * 256, ad + k * kStepA, bd + k * kStepB, idesc, (i > t.k0 || k > 0) ? 1u : 0u);
-        tc_commit_all<2>(&sm.empty[stage]);
+        pair_commit(sm, &sm.empty[stage]);
       }
       if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1;
       }
     }
-    if (elect_one()) tc_commit_all<2>(&sm.accf[acc]);
+    if (elect_one()) pair_commit(sm, &sm.accf[acc]);
   }
   return true;
 }
@@ -566,7 +587,8 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
     // (every TMEM read of this warp has been waited for)
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_leader<2>(&sm.acce[acc]);
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(pair_leader(sm, &sm.acce[acc])) : "memory");
   }
   return true;
 }
@@ -593,7 +615,8 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
   sm.abort_flag = reinterpret_cast<volatile int*>(sm.base + C::kOffMisc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = cluster_ctarank() & 1;
+  sm.pair = cluster_ctarank() & ~1u;
   const bool leader = rank == 0;
   const int cluster_id = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   const int products = 3 * p.steps;
@@ -626,22 +649,35 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
   cluster_or_block_sync<2>();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
 
+  // Between two products every CTA's results reach memory.  In one cluster every
+  // warp arrives at the cluster's barrier when it has done its share and waits
+  // there before the next (one that has given up a wait keeps doing both, so
+  // that the others are not held); else the epilogues count a CTA's arrival in
+  // memory and the producers wait for the count.
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_phase = 0;
+    bool ok = true;
     for (int i = 0; i < products; ++i) {
       if (i > 0) {
-        // every CTA's results of the product before are in memory
-        bool ok = true;
-        if (lane == 0) ok = count_wait(p.grid_count, (uint32_t)i * gridDim.x, sm.abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        fence_proxy_async_all();
-        if (lane == 0) mbar_arrive(sm.ready);
+        if (p.one_cluster) {
+          __syncwarp();
+          cluster_arrive();
+          cluster_wait();
+          fence_proxy_async_all();
+        } else {
+          if (lane == 0) ok = count_wait(p.grid_count, (uint32_t)i * gridDim.x, sm.abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          fence_proxy_async_all();
+          if (lane == 0) mbar_arrive(sm.ready);
+        }
       }
+      if (!ok) continue;
       const int type = i % 3, cur = (i / 3) & 1;
-      bool ok;
       if (type == kOrthoGram)
         ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram_b[cur][0],
                                           &m.gram_b[cur][1], cluster_id, clusters, rank, stage, phase, issued,
@@ -655,7 +691,7 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
       else
         ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
                                             cluster_id, clusters, rank, stage, phase, issued, issued_phase);
-      if (!ok) break;
+      if (!ok && !p.one_cluster) break;
     }
     // let every load of the pair land before the leader can exit
     if (lane == 0 && leader) {
@@ -671,31 +707,48 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
     if (leader) {
       int stage = 0;
       uint32_t phase = 0, it = 0;
+      bool ok = true;
       for (int i = 0; i < products; ++i) {
+        if (i > 0 && p.one_cluster) {
+          __syncwarp();
+          cluster_arrive();
+          cluster_wait();
+        }
+        if (!ok) continue;
         const int type = i % 3;
-        bool ok;
         if (type == kOrthoGram)
           ok = ortho_mma<true, TALL, TALL>(sm, p.shape[kOrthoGram], tmem, cluster_id, clusters, stage, phase, it);
         else if (type == kOrthoPoly)
           ok = ortho_mma<true, false, false>(sm, p.shape[kOrthoPoly], tmem, cluster_id, clusters, stage, phase, it);
         else
           ok = ortho_mma<false, false, !TALL>(sm, p.shape[kOrthoUpdate], tmem, cluster_id, clusters, stage, phase, it);
-        if (!ok) break;
+        if (!ok && !p.one_cluster) break;
       }
       if (elect_one()) tc_commit_local<2>(sm.drain);
       volatile int no_abort = 0;
       mbar_wait(sm.drain, 0, &no_abort, 100000000ull);
       __syncwarp();
+    } else if (p.one_cluster) {
+      for (int i = 1; i < products; ++i) {
+        cluster_arrive();
+        cluster_wait();
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     OrthoEpiState st = {0, 0, 0, 0};
+    bool ok = true;
     for (int i = 0; i < products; ++i) {
       const int type = i % 3, step = i / 3, cur = step & 1;
-      if (i > 0 && !mbar_wait_warp(sm.ready, (uint32_t)(i - 1) & 1, sm.abort_flag)) break;
-      fence_proxy_async_all();
-      bool ok;
-      if (type == kOrthoGram)
+      if (i > 0) {
+        if (p.one_cluster)
+          cluster_wait();
+        else if (!mbar_wait_warp(sm.ready, (uint32_t)(i - 1) & 1, sm.abort_flag))
+          break;
+        fence_proxy_async_all();
+      }
+      if (!ok) {
+      } else if (type == kOrthoGram)
         ok = ortho_epilogue<kOrthoGram, TALL>(sm, p, nullptr, nullptr, &m.eo, &m.eo, tmem, cluster_id, clusters, rank,
                                               step, st);
       else if (type == kOrthoPoly)
@@ -705,13 +758,18 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
         ok = ortho_epilogue<kOrthoUpdate, TALL>(sm, p, &m.ex[cur][0], &m.ex[cur][1],
                                                 step == p.steps - 1 ? &m.out : &m.ex[cur ^ 1][0], &m.ex[cur ^ 1][1],
                                                 tmem, cluster_id, clusters, rank, step, st);
-      if (!ok || i == products - 1) break;
-      // this CTA's results are in memory: one arrival at the grid's barrier
+      if (i == products - 1 || (!ok && !p.one_cluster)) break;
+      // this warp's results are in memory
       if (lane == 0) {
         bulk_wait_group<0>();
         fence_proxy_async_all();
       }
       __syncwarp();
+      if (p.one_cluster) {
+        cluster_arrive();
+        continue;
+      }
+      // all of this CTA's: one arrival at the grid's barrier
       if (lane == 0) mbar_arrive(sm.done);
       if (warp == 2) {
         if (!mbar_wait_warp(sm.done, (uint32_t)i & 1, sm.abort_flag)) break;
