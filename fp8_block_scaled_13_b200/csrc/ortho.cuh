@@ -26,11 +26,11 @@
 // times 2^12, which holds while |X| < 64, |M| < 8 and |R| < 16 off the
 // diagonal; the iteration keeps singular values near 1.
 //
-// A whole call is one cooperative launch after two passes over G (its norm, and
-// the two FP16 terms of X0).  Its 3 * steps products D[i, j] = sum_k A[i, k]
-// B[j, k] follow each other over a barrier of the grid's CTAs: the next
-// product's loads wait for it, everything else (TMEM, barriers, tensor maps)
-// stays set up.  (One launch per product took 3.8 us each in tails and starts;
+// A whole call is one launch after two passes over G (its norm, and the two FP16
+// terms of X0).  Its 3 * steps products D[i, j] = sum_k A[i, k] B[j, k] follow
+// each other over a barrier -- of the cluster, where the grid is one, else of a
+// cooperative grid's CTAs through memory: the next product's loads wait for it,
+// everything else (TMEM, barriers, tensor maps) stays set up.  (One launch per product took 3.8 us each in tails and starts;
 // with 128-column tiles and without the split below: 313 us against 267 for
 // 2048 x 2048, 1133 against 800 to 950, by the power cap, for 12288 x 2048.)
 //

@@ -399,8 +399,8 @@ PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
  * product is rounded to FP16 off the diagonal, and out to BF16 once.
  * 1 <= n, k <= 65536 (0: no-op); 1 <= steps <= 64; eps >= 0; coefficients that
  * let a singular value from [0, 1] reach 2 are refused (PURO_ERR_SHAPE).
- * The products run as one cooperative launch, which waits until all its CTAs
- * fit on the device beside what else runs there.
+ * Large gradients take a cooperative launch, which waits until all its CTAs fit
+ * on the device beside what else runs there; small ones a single cluster.
  */
 PURO_API int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, int64_t n, int64_t k,
                                     int steps, float a, float b, float c, float eps, void* out,
