@@ -441,16 +441,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_backward_kerne
       gt[k] = row_in && p.gate_kind == kGateToken ? load_param(p.gate, p.gate_f32, r) : 1.f;
     }
     cp_async_wait<1>();
-    const uint8_t* src = ring + ((rb / ROWS) & 1) * ROWS * tensors * pitch + threadIdx.x * 16;
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
+    const uint8_t* stage = ring + ((rb / ROWS) & 1) * ROWS * tensors * pitch + threadIdx.x * 16;
+    auto read = [&](int k) {
+      const uint8_t* src = stage + k * tensors * pitch;
       nv[k] = lds_v4(src);
       yv[k] = lds_v4(src += pitch);
       gv[k] = p.dy ? lds_v4(src += pitch) : zero;
       hv[k] = p.h ? lds_v4(src += pitch) : zero;
       tv[k] = p.gate_kind == kGateFull ? lds_v4(src += pitch) : zero;
-      src += pitch;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) read(k);
     float sum[3 * ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -487,8 +488,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_backward_kerne
       sum[3 * k + 2] = f2_sum(sq);
     }
     row_sums<ROWS>(sum, red, buf);
-    // (every load from this stage has been used in the sums by now)
-    fetch(rb + 2 * ROWS);
+    // (1024 threads have 64 registers each, too few to keep the rows over the
+    // barrier: they read them again, 8192 x 8192 in 267 us against 298)
+    if (MAXT == 1024) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        asm volatile("" ::: "memory");
+        read(k);
+      }
+    } else {
+      // (every load from this stage has been used in the sums by now)
+      fetch(rb + 2 * ROWS);
+    }
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int64_t r = row0 + rb + k;
@@ -525,6 +536,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_backward_kerne
       out[k] = pack8(h);
       if (p.out.bf && in) *reinterpret_cast<uint4*>(p.out.bf + r * p.out.ld_bf + col) = out[k];
     }
+    if (MAXT == 1024) fetch(rb + 2 * ROWS);  // (the rows read again have been used)
     if (p.out.q) {
 #pragma unroll
       for (int k = 0; k < ROWS; k += 2)
