@@ -255,57 +255,60 @@ __device__ __forceinline__ void pair_commit(const OrthoSmem& sm, uint64_t* bar) 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The producer warp's share of one product.
+// The producer's share of one product, by one thread.  `blocks` counts the
+// 64-deep blocks so far: block n goes through stage n % kStages.  (One thread
+// that runs the whole loop takes 150 cycles a block, a warp that elects a lane
+// in every round 470: as long as the products of 256 columns and twice as long
+// as those of 128.)
 template <bool SYM, bool AMN, bool BMN>
 __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape& s, const CUtensorMap* ah,
                                            const CUtensorMap* al, const CUtensorMap* bh, const CUtensorMap* bl,
-                                           int cluster_id, int clusters, uint32_t rank, int& stage, uint32_t& phase,
-                                           uint32_t& issued, uint32_t& issued_phase) {
+                                           int cluster_id, int clusters, uint32_t rank, uint32_t& blocks) {
   using C = OrthoCfg;
   // both CTAs' bytes of a stage
   const uint32_t bytes = 2 * (C::kTile + (BMN ? (s.bn == 256 ? 16384u : 8192u) : (uint32_t)s.bn * 64));
+  const uint32_t full0 = pair_leader(sm, sm.full);
+  const bool wide = s.bn == 256;
   for (int32_t u = cluster_id; u < s.units; u += clusters) {
     const OrthoUnit t = ortho_unit<SYM>(s, u);
     const int32_t a0 = t.y0 + 128 * (int32_t)rank;
     const int32_t b0 = t.x0 + (t.cols >> 1) * (int32_t)rank;
-    for (int32_t i = t.k0; i < t.k1; ++i) {
-      const int32_t pass = s.passes == 1 ? 0 : i / s.kblocks, k = (i - pass * s.kblocks) * 64;
-      if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1, sm.abort_flag)) return false;
-      if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], bytes);
-        const uint32_t bar = pair_leader(sm, &sm.full[stage]);
-        uint8_t* da = sm.base + stage * C::kStageBytes;
-        uint8_t* db = da + C::kTile;
-        const CUtensorMap* ma = pass == 2 ? al : ah;
-        const CUtensorMap* mb = pass == 1 ? bl : bh;
-        if (AMN) {
-          tma_load_2d<2>(da, ma, a0, k, bar);
-          tma_load_2d<2>(da + 8192, ma, a0 + 64, k, bar);
-        } else {
-          tma_load_2d<2>(da, ma, k, a0, bar);
-        }
-        if (BMN) {
-          tma_load_2d<2>(db, mb, b0, k, bar);
-          if (s.bn == 256) tma_load_2d<2>(db + 8192, mb, b0 + 64, k, bar);
-        } else {
-          tma_load_2d<2>(db, mb, k, b0, bar);
-        }
+    int32_t pass = s.passes == 1 ? 0 : t.k0 / s.kblocks, k = (t.k0 - pass * s.kblocks) * 64;
+    for (int32_t n = t.k1 - t.k0; n > 0; --n, ++blocks) {
+      const uint32_t stage = blocks % C::kStages;
+      if (!mbar_wait(&sm.empty[stage], (blocks / C::kStages & 1) ^ 1, sm.abort_flag)) return false;
+      if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], bytes);
+      const uint32_t bar = full0 + stage * 8;
+      uint8_t* da = sm.base + stage * C::kStageBytes;
+      uint8_t* db = da + C::kTile;
+      const CUtensorMap* ma = pass == 2 ? al : ah;
+      const CUtensorMap* mb = pass == 1 ? bl : bh;
+      if (AMN) {
+        tma_load_2d<2>(da, ma, a0, k, bar);
+        tma_load_2d<2>(da + 8192, ma, a0 + 64, k, bar);
+      } else {
+        tma_load_2d<2>(da, ma, k, a0, bar);
       }
-      issued |= 1u << stage;
-      issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-      if (++stage == C::kStages) {
-        stage = 0;
-        phase ^= 1;
+      if (BMN) {
+        tma_load_2d<2>(db, mb, b0, k, bar);
+        if (wide) tma_load_2d<2>(db + 8192, mb, b0 + 64, k, bar);
+      } else {
+        tma_load_2d<2>(db, mb, k, b0, bar);
+      }
+      k += 64;
+      if (k >= s.kblocks * 64) {
+        k = 0;
+        ++pass;
       }
     }
   }
   return true;
 }
 
-// The MMA warp's (leader CTA only).
+// The MMA issuer's, by one thread of the leader CTA.
 template <bool SYM, bool AMN, bool BMN>
 __device__ __forceinline__ bool ortho_mma(const OrthoSmem& sm, const OrthoShape& s, uint32_t tmem, int cluster_id,
-                                          int clusters, int& stage, uint32_t& phase, uint32_t& it) {
+                                          int clusters, uint32_t& blocks, uint32_t& it) {
   using C = OrthoCfg;
   constexpr uint32_t kStepA = AMN ? 2048 >> 4 : 32 >> 4;  // 16 elements along k
   constexpr uint32_t kStepB = BMN ? 2048 >> 4 : 32 >> 4;
@@ -318,25 +321,20 @@ __device__ __forceinline__ bool ortho_mma(const OrthoSmem& sm, const OrthoShape&
     const uint32_t idesc = (1u << 4) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
                            ((uint32_t)(t.cols >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
     const uint32_t acc = it & 1;
-    if (!mbar_wait_warp(&sm.acce[acc], ((it >> 1) & 1) ^ 1, sm.abort_flag)) return false;
+    if (!mbar_wait(&sm.acce[acc], ((it >> 1) & 1) ^ 1, sm.abort_flag)) return false;
     tc_fence_after();
-    for (int32_t i = t.k0; i < t.k1; ++i) {
-      if (!mbar_wait_warp(&sm.full[stage], phase, sm.abort_flag)) return false;
+    for (int32_t n = t.k1 - t.k0; n > 0; --n, ++blocks) {
+      const uint32_t stage = blocks % C::kStages;
+      if (!mbar_wait(&sm.full[stage], blocks / C::kStages & 1, sm.abort_flag)) return false;
       tc_fence_after();
-      if (elect_one()) {
-        const uint64_t ad = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
-        const uint64_t bd = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+      const uint64_t ad = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+      const uint64_t bd = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_f16(tmem + acc * 256, ad + k * kStepA, bd + k * kStepB, idesc, (i > t.k0 || k > 0) ? 1u : 0u);
-        pair_commit(sm, &sm.empty[stage]);
-      }
-      if (++stage == C::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
+      for (int k = 0; k < 4; ++k)
+        tc_mma_f16(tmem + acc * 256, ad + k * kStepA, bd + k * kStepB, idesc, (n < t.k1 - t.k0 || k > 0) ? 1u : 0u);
+      pair_commit(sm, &sm.empty[stage]);
     }
-    if (elect_one()) pair_commit(sm, &sm.accf[acc]);
+    pair_commit(sm, &sm.accf[acc]);
   }
   return true;
 }
@@ -658,8 +656,7 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
   // memory and the producers wait for the count.
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    uint32_t blocks = 0;  // of the elected lane, which is the same every time
     bool ok = true;
     for (int i = 0; i < products; ++i) {
       if (i > 0) {
@@ -678,35 +675,35 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
       }
       if (!ok) continue;
       const int type = i % 3, cur = (i / 3) & 1;
-      if (type == kOrthoGram)
-        ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram_b[cur][0],
-                                          &m.gram_b[cur][1], cluster_id, clusters, rank, stage, phase, issued,
-                                          issued_phase);
-      else if (type == kOrthoPoly)
-        ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o_b, &m.o_b, cluster_id, clusters, rank,
-                                            stage, phase, issued, issued_phase);
-      else if (TALL)
-        ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,
-                                             cluster_id, clusters, rank, stage, phase, issued, issued_phase);
-      else
-        ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
-                                            cluster_id, clusters, rank, stage, phase, issued, issued_phase);
+      if (elect_one()) {
+        if (type == kOrthoGram)
+          ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram_b[cur][0],
+                                            &m.gram_b[cur][1], cluster_id, clusters, rank, blocks);
+        else if (type == kOrthoPoly)
+          ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o_b, &m.o_b, cluster_id, clusters,
+                                              rank, blocks);
+        else if (TALL)
+          ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,
+                                               cluster_id, clusters, rank, blocks);
+        else
+          ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
+                                              cluster_id, clusters, rank, blocks);
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok && !p.one_cluster) break;
     }
     // let every load of the pair land before the leader can exit
-    if (lane == 0 && leader) {
-      for (int s = 0; s < S; ++s)
-        if (issued & (1u << s)) {
-          volatile int no_abort = 0;
-          mbar_wait(&sm.full[s], (issued_phase >> s) & 1u, &no_abort, 100000000ull);
-        }
+    if (leader && elect_one()) {
+      for (uint32_t n = blocks < S ? 0 : blocks - S; n < blocks; ++n) {
+        volatile int no_abort = 0;
+        mbar_wait(&sm.full[n % S], n / S & 1, &no_abort, 100000000ull);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (leader) {
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
+      uint32_t blocks = 0, it = 0;  // of the elected lane
       bool ok = true;
       for (int i = 0; i < products; ++i) {
         if (i > 0 && p.one_cluster) {
@@ -716,12 +713,15 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
         }
         if (!ok) continue;
         const int type = i % 3;
-        if (type == kOrthoGram)
-          ok = ortho_mma<true, TALL, TALL>(sm, p.shape[kOrthoGram], tmem, cluster_id, clusters, stage, phase, it);
-        else if (type == kOrthoPoly)
-          ok = ortho_mma<true, false, false>(sm, p.shape[kOrthoPoly], tmem, cluster_id, clusters, stage, phase, it);
-        else
-          ok = ortho_mma<false, false, !TALL>(sm, p.shape[kOrthoUpdate], tmem, cluster_id, clusters, stage, phase, it);
+        if (elect_one()) {
+          if (type == kOrthoGram)
+            ok = ortho_mma<true, TALL, TALL>(sm, p.shape[kOrthoGram], tmem, cluster_id, clusters, blocks, it);
+          else if (type == kOrthoPoly)
+            ok = ortho_mma<true, false, false>(sm, p.shape[kOrthoPoly], tmem, cluster_id, clusters, blocks, it);
+          else
+            ok = ortho_mma<false, false, !TALL>(sm, p.shape[kOrthoUpdate], tmem, cluster_id, clusters, blocks, it);
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok && !p.one_cluster) break;
       }
       if (elect_one()) tc_commit_local<2>(sm.drain);
