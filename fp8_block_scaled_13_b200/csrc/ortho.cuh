@@ -156,24 +156,28 @@ struct OrthoUnit {
 template <bool SYM>
 __device__ __forceinline__ OrthoUnit ortho_unit(const OrthoShape& s, int32_t u) {
   OrthoUnit r;
-  const int32_t total = s.kblocks * s.passes;
+  const uint32_t total = s.kblocks * s.passes;  // (times a part fits 32 bits: 2^25 blocks at most)
   int32_t t = u;
   r.part = 0;
   r.parts = 1;
   r.index = 0;
-  if (u >= s.full) {
-    r.index = (u - s.full) / s.split;
-    r.part = u - s.full - r.index * s.split;
+  r.k0 = 0;
+  r.k1 = (int32_t)total;
+  if (s.split > 1 && u >= s.full) {
+    const uint32_t split = s.split, rest = u - s.full;
+    r.index = (int32_t)(rest / split);
+    r.part = (int32_t)(rest % split);
     r.parts = s.split;
     t = s.full + r.index;
+    r.k0 = (int32_t)(total * r.part / split);
+    r.k1 = (int32_t)(total * (r.part + 1) / split);
   }
-  r.k0 = (int32_t)((int64_t)total * r.part / r.parts);
-  r.k1 = (int32_t)((int64_t)total * (r.part + 1) / r.parts);
   int32_t tm, tn;
   if (SYM) {
     // row by row of tiles that reach the diagonal's 256 x 256 blocks or lie below
+    const int32_t per = s.bn == 256 ? 1 : s.bn == 128 ? 2 : 4;
     for (tm = 0;; ++tm) {
-      const int32_t to_diag = (tm + 1) * (256 / s.bn), n = to_diag < s.tiles_n ? to_diag : s.tiles_n;
+      const int32_t to_diag = (tm + 1) * per, n = to_diag < s.tiles_n ? to_diag : s.tiles_n;
       if (t < n) break;
       t -= n;
     }
@@ -181,10 +185,10 @@ __device__ __forceinline__ OrthoUnit ortho_unit(const OrthoShape& s, int32_t u) 
   } else if (s.tiles_n < s.tiles_m) {
     // along the shorter side of D first, so that tiles that run at the same
     // time share their part of X
-    tm = t / s.tiles_n;
+    tm = (int32_t)((uint32_t)t / (uint32_t)s.tiles_n);
     tn = t - tm * s.tiles_n;
   } else {
-    tn = t / s.tiles_m;
+    tn = s.tiles_m == 1 ? t : (int32_t)((uint32_t)t / (uint32_t)s.tiles_m);
     tm = t - tn * s.tiles_m;
   }
   r.y0 = tm * 256;
@@ -204,6 +208,7 @@ __device__ __forceinline__ float2 half_unpack(uint32_t w) {
 }
 
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 __device__ __forceinline__ void count_arrive(uint32_t* c) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c) : "memory");
@@ -257,9 +262,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // The producer's share of one product, by one thread.  `blocks` counts the
 // 64-deep blocks so far: block n goes through stage n % kStages.  (One thread
-// that runs the whole loop takes 150 cycles a block, a warp that elects a lane
-// in every round 470: as long as the products of 256 columns and twice as long
-// as those of 128.)
+// that runs the whole loop takes 300 cycles a block, a warp that elects a lane
+// in every round 470: nearly as long as the products of 256 columns, and twice
+// as long as those of 128.  Unrolling the stages and looking at the next
+// barrier ahead brought nothing.)
 template <bool SYM, bool AMN, bool BMN>
 __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape& s, const CUtensorMap* ah,
                                            const CUtensorMap* al, const CUtensorMap* bh, const CUtensorMap* bl,
@@ -273,7 +279,7 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
     const OrthoUnit t = ortho_unit<SYM>(s, u);
     const int32_t a0 = t.y0 + 128 * (int32_t)rank;
     const int32_t b0 = t.x0 + (t.cols >> 1) * (int32_t)rank;
-    int32_t pass = s.passes == 1 ? 0 : t.k0 / s.kblocks, k = (t.k0 - pass * s.kblocks) * 64;
+    int32_t pass = s.passes == 1 || t.k0 == 0 ? 0 : t.k0 / s.kblocks, k = (t.k0 - pass * s.kblocks) * 64;
     for (int32_t n = t.k1 - t.k0; n > 0; --n, ++blocks) {
       const uint32_t stage = blocks % C::kStages;
       if (!mbar_wait(&sm.empty[stage], (blocks / C::kStages & 1) ^ 1, sm.abort_flag)) return false;
@@ -664,12 +670,12 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
           __syncwarp();
           cluster_arrive();
           cluster_wait();
-          fence_proxy_async_all();
+          fence_proxy_async_global();
         } else {
           if (lane == 0) ok = count_wait(p.grid_count, (uint32_t)i * gridDim.x, sm.abort_flag);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-          fence_proxy_async_all();
+          fence_proxy_async_global();
           if (lane == 0) mbar_arrive(sm.ready);
         }
       }
@@ -745,7 +751,7 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
           cluster_wait();
         else if (!mbar_wait_warp(sm.ready, (uint32_t)(i - 1) & 1, sm.abort_flag))
           break;
-        fence_proxy_async_all();
+        fence_proxy_async_global();
       }
       if (!ok) {
       } else if (type == kOrthoGram)
@@ -760,10 +766,7 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
                                                 tmem, cluster_id, clusters, rank, step, st);
       if (i == products - 1 || (!ok && !p.one_cluster)) break;
       // this warp's results are in memory
-      if (lane == 0) {
-        bulk_wait_group<0>();
-        fence_proxy_async_all();
-      }
+      if (lane == 0) bulk_wait_group<0>();
       __syncwarp();
       if (p.one_cluster) {
         cluster_arrive();
