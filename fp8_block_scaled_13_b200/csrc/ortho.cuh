@@ -125,17 +125,6 @@ struct OrthoCfg {
   static constexpr uint32_t kTmemCols = 512;          // two accumulators
 };
 
-// D[tmem] (+)= A B^T for one M = 256, K = 16 slice of FP16 operands of the CTA pair.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Shared-memory matrix descriptor of an MN-major operand tile: 128-byte
 // swizzled rows of 64 elements, one row per k; 8-row groups 1024 B apart
 // (stride offset), 64-element column blocks of 64 rows 8192 B apart (leading
@@ -249,10 +238,10 @@ __device__ __forceinline__ uint32_t pair_leader(const OrthoSmem& sm, const void*
 }
 
 // Arrive on `bar` in both CTAs of the pair when the MMAs issued so far are done.
-__device__ __forceinline__ void pair_commit(const OrthoSmem& sm, uint64_t* bar) {
+__device__ __forceinline__ void pair_commit(const OrthoSmem& sm, uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
+          bar),
       "h"((uint16_t)(3u << sm.pair))
       : "memory");
 }
@@ -260,87 +249,131 @@ __device__ __forceinline__ void pair_commit(const OrthoSmem& sm, uint64_t* bar) 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The producer's share of one product, by one thread.  `blocks` counts the
-// 64-deep blocks so far: block n goes through stage n % kStages.  (One thread
-// that runs the whole loop takes 300 cycles a block, a warp that elects a lane
-// in every round 470: nearly as long as the products of 256 columns, and twice
-// as long as those of 128.  Unrolling the stages and looking at the next
-// barrier ahead brought nothing.)
-template <bool SYM, bool AMN, bool BMN>
+// The loops below run in one thread each: a warp that elected a lane in every
+// round took 470 cycles a 64-deep block, nearly as long as the products of 256
+// columns and twice as long as those of 128 (1024 x 1024: 171 us against 151).
+// A single thread's time is the number of its instructions, so addresses are
+// 32-bit shared-memory ones and a descriptor's upper half stays constant.
+
+__device__ __forceinline__ void ortho_tma(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// The producer's share of one product.  `blocks` counts the 64-deep blocks so
+// far: block n goes through stage n % kStages.  What can be computed before the
+// operands are there comes before `arrived`, the barrier between the products.
+template <bool SYM, bool AMN, bool BMN, class Barrier>
 __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape& s, const CUtensorMap* ah,
                                            const CUtensorMap* al, const CUtensorMap* bh, const CUtensorMap* bl,
-                                           int cluster_id, int clusters, uint32_t rank, uint32_t& blocks) {
+                                           int cluster_id, int clusters, uint32_t rank, uint32_t& blocks,
+                                           const Barrier& arrived) {
   using C = OrthoCfg;
   // both CTAs' bytes of a stage
   const uint32_t bytes = 2 * (C::kTile + (BMN ? (s.bn == 256 ? 16384u : 8192u) : (uint32_t)s.bn * 64));
-  const uint32_t full0 = pair_leader(sm, sm.full);
+  const uint32_t full = smem_u32(sm.full), empty = smem_u32(sm.empty), base = smem_u32(sm.base);
+  const uint32_t to_leader = pair_leader(sm, sm.full) - full;
   const bool wide = s.bn == 256;
-  for (int32_t u = cluster_id; u < s.units; u += clusters) {
-    const OrthoUnit t = ortho_unit<SYM>(s, u);
-    const int32_t a0 = t.y0 + 128 * (int32_t)rank;
-    const int32_t b0 = t.x0 + (t.cols >> 1) * (int32_t)rank;
-    int32_t pass = s.passes == 1 || t.k0 == 0 ? 0 : t.k0 / s.kblocks, k = (t.k0 - pass * s.kblocks) * 64;
-    for (int32_t n = t.k1 - t.k0; n > 0; --n, ++blocks) {
-      const uint32_t stage = blocks % C::kStages;
-      if (!mbar_wait(&sm.empty[stage], (blocks / C::kStages & 1) ^ 1, sm.abort_flag)) return false;
-      if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], bytes);
-      const uint32_t bar = full0 + stage * 8;
-      uint8_t* da = sm.base + stage * C::kStageBytes;
-      uint8_t* db = da + C::kTile;
+  const int32_t k_end = s.kblocks * 64;
+  OrthoUnit t = ortho_unit<SYM>(s, cluster_id < s.units ? cluster_id : 0);
+  if (!arrived()) return false;
+  auto loop = [&]() {
+    for (int32_t u = cluster_id; u < s.units;) {
+      const int32_t a0 = t.y0 + 128 * (int32_t)rank;
+      const int32_t b0 = t.x0 + (t.cols >> 1) * (int32_t)rank;
+      int32_t pass = s.passes == 1 || t.k0 == 0 ? 0 : t.k0 / s.kblocks, k = (t.k0 - pass * s.kblocks) * 64;
       const CUtensorMap* ma = pass == 2 ? al : ah;
       const CUtensorMap* mb = pass == 1 ? bl : bh;
-      if (AMN) {
-        tma_load_2d<2>(da, ma, a0, k, bar);
-        tma_load_2d<2>(da + 8192, ma, a0 + 64, k, bar);
-      } else {
-        tma_load_2d<2>(da, ma, k, a0, bar);
+      for (int32_t n = t.k1 - t.k0; n > 0; --n) {
+        const uint32_t stage = blocks % C::kStages, odd = blocks / C::kStages & 1, at = full + stage * 8;
+        ++blocks;
+        if (!mbar_try_wait(empty + stage * 8, odd ^ 1) && !mbar_wait(&sm.empty[stage], odd ^ 1, sm.abort_flag))
+          return false;
+        if (rank == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(at), "r"(bytes) : "memory");
+        const uint32_t bar = at + to_leader, da = base + stage * C::kStageBytes, db = da + C::kTile;
+        if (AMN) {
+          ortho_tma(da, ma, a0, k, bar);
+          ortho_tma(da + 8192, ma, a0 + 64, k, bar);
+        } else {
+          ortho_tma(da, ma, k, a0, bar);
+        }
+        if (BMN) {
+          ortho_tma(db, mb, b0, k, bar);
+          if (wide) ortho_tma(db + 8192, mb, b0 + 64, k, bar);
+        } else {
+          ortho_tma(db, mb, k, b0, bar);
+        }
+        k += 64;
+        if (SYM && k >= k_end) {
+          k = 0;
+          ++pass;
+          ma = pass == 2 ? al : ah;
+          mb = pass == 1 ? bl : bh;
+        }
       }
-      if (BMN) {
-        tma_load_2d<2>(db, mb, b0, k, bar);
-        if (wide) tma_load_2d<2>(db + 8192, mb, b0 + 64, k, bar);
-      } else {
-        tma_load_2d<2>(db, mb, k, b0, bar);
-      }
-      k += 64;
-      if (k >= s.kblocks * 64) {
-        k = 0;
-        ++pass;
-      }
+      u += clusters;
+      if (u < s.units) t = ortho_unit<SYM>(s, u);
     }
-  }
-  return true;
+    return true;
+  };
+  const bool ok = elect_one() ? loop() : true;
+  return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// The MMA issuer's, by one thread of the leader CTA.
+// D[tmem] (+)= A B^T for one M = 256, K = 16 slice of FP16 operands of the CTA pair;
+// a and b are the descriptors' lower halves; the upper one says the same of both
+// layouts (groups 1024 bytes apart, 128-byte swizzle).
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t"
+      "}" ::"r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"((1024 >> 4) | (1 << 14) | (2 << 29))
+      : "memory");
+}
+
+// The MMA issuer's, in the leader CTA.
 template <bool SYM, bool AMN, bool BMN>
 __device__ __forceinline__ bool ortho_mma(const OrthoSmem& sm, const OrthoShape& s, uint32_t tmem, int cluster_id,
                                           int clusters, uint32_t& blocks, uint32_t& it) {
   using C = OrthoCfg;
   constexpr uint32_t kStepA = AMN ? 2048 >> 4 : 32 >> 4;  // 16 elements along k
   constexpr uint32_t kStepB = BMN ? 2048 >> 4 : 32 >> 4;
-  const uint32_t base = smem_u32(sm.base);
-  const uint64_t a_desc0 = AMN ? desc_sw128_mnmajor(base) : desc_sw128_kmajor(base);
-  const uint64_t b_desc0 = BMN ? desc_sw128_mnmajor(base + C::kTile) : desc_sw128_kmajor(base + C::kTile);
+  const uint64_t a_desc0 = AMN ? desc_sw128_mnmajor(smem_u32(sm.base)) : desc_sw128_kmajor(smem_u32(sm.base));
+  const uint64_t b_desc0 = BMN ? desc_sw128_mnmajor(smem_u32(sm.base) + C::kTile)
+                               : desc_sw128_kmajor(smem_u32(sm.base) + C::kTile);
+  const uint32_t a_lo = (uint32_t)a_desc0, b_lo = (uint32_t)b_desc0;
+  const uint32_t full = smem_u32(sm.full), empty = smem_u32(sm.empty);
   for (int32_t u = cluster_id; u < s.units; u += clusters, ++it) {
     const OrthoUnit t = ortho_unit<SYM>(s, u);
     // D FP32, A and B FP16 (formats 0), MN-major flags, N, M
     const uint32_t idesc = (1u << 4) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
                            ((uint32_t)(t.cols >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-    const uint32_t acc = it & 1;
+    const uint32_t acc = it & 1, d = tmem + acc * 256;
     if (!mbar_wait(&sm.acce[acc], ((it >> 1) & 1) ^ 1, sm.abort_flag)) return false;
     tc_fence_after();
-    for (int32_t n = t.k1 - t.k0; n > 0; --n, ++blocks) {
-      const uint32_t stage = blocks % C::kStages;
-      if (!mbar_wait(&sm.full[stage], blocks / C::kStages & 1, sm.abort_flag)) return false;
+    uint32_t accumulate = 0;
+    for (int32_t n = t.k1 - t.k0; n > 0; --n) {
+      const uint32_t stage = blocks % C::kStages, odd = blocks / C::kStages & 1;
+      ++blocks;
+      if (!mbar_try_wait(full + stage * 8, odd) && !mbar_wait(&sm.full[stage], odd, sm.abort_flag)) return false;
       tc_fence_after();
-      const uint64_t ad = a_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
-      const uint64_t bd = b_desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+      const uint32_t a = a_lo + stage * (C::kStageBytes >> 4), b = b_lo + stage * (C::kStageBytes >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma_f16(tmem + acc * 256, ad + k * kStepA, bd + k * kStepB, idesc, (n < t.k1 - t.k0 || k > 0) ? 1u : 0u);
-      pair_commit(sm, &sm.empty[stage]);
+      for (int k = 0; k < 4; ++k) {
+        tc_mma_f16(d, a + k * kStepA, b + k * kStepB, idesc, accumulate);
+        accumulate = 1;
+      }
+      pair_commit(sm, empty + stage * 8);
     }
-    pair_commit(sm, &sm.accf[acc]);
+    pair_commit(sm, smem_u32(&sm.accf[acc]));
   }
   return true;
 }
@@ -665,37 +698,39 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
     uint32_t blocks = 0;  // of the elected lane, which is the same every time
     bool ok = true;
     for (int i = 0; i < products; ++i) {
-      if (i > 0) {
+      if (i > 0 && p.one_cluster) {
+        __syncwarp();
+        cluster_arrive();
+      }
+      auto arrived = [&]() {
+        if (i == 0) return true;
         if (p.one_cluster) {
-          __syncwarp();
-          cluster_arrive();
           cluster_wait();
           fence_proxy_async_global();
-        } else {
-          if (lane == 0) ok = count_wait(p.grid_count, (uint32_t)i * gridDim.x, sm.abort_flag);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          fence_proxy_async_global();
-          if (lane == 0) mbar_arrive(sm.ready);
+          return true;
         }
-      }
-      if (!ok) continue;
+        bool here = true;
+        if (lane == 0) here = count_wait(p.grid_count, (uint32_t)i * gridDim.x, sm.abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, here)) return false;
+        fence_proxy_async_global();
+        if (lane == 0) mbar_arrive(sm.ready);
+        return true;
+      };
       const int type = i % 3, cur = (i / 3) & 1;
-      if (elect_one()) {
-        if (type == kOrthoGram)
-          ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram_b[cur][0],
-                                            &m.gram_b[cur][1], cluster_id, clusters, rank, blocks);
-        else if (type == kOrthoPoly)
-          ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o_b, &m.o_b, cluster_id, clusters,
-                                              rank, blocks);
-        else if (TALL)
-          ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,
-                                               cluster_id, clusters, rank, blocks);
-        else
-          ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
-                                              cluster_id, clusters, rank, blocks);
-      }
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok)
+        arrived();  // (one cluster: the others still wait for this warp)
+      else if (type == kOrthoGram)
+        ok = ortho_load<true, TALL, TALL>(sm, p.shape[kOrthoGram], &m.gram[cur][0], &m.gram[cur][1], &m.gram_b[cur][0],
+                                          &m.gram_b[cur][1], cluster_id, clusters, rank, blocks, arrived);
+      else if (type == kOrthoPoly)
+        ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o_b, &m.o_b, cluster_id, clusters,
+                                            rank, blocks, arrived);
+      else if (TALL)
+        ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,
+                                             cluster_id, clusters, rank, blocks, arrived);
+      else
+        ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
+                                            cluster_id, clusters, rank, blocks, arrived);
       if (!ok && !p.one_cluster) break;
     }
     // let every load of the pair land before the leader can exit
