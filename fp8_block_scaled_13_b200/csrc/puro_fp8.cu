@@ -1228,16 +1228,16 @@ constexpr int64_t kOrthoMaxDim = 65536;
 // pairs a split along k, that together should take the least time.  In cycles,
 // measured on a B200: a 64-deep block of a tile, by its width; 32 columns of an
 // epilogue, which two sets of warps share; a split tile's hand-over, and writing
-// and reading 32 columns of partials.  (200 x 333: 125 us against 166 with 256
-// columns throughout, 512 x 512: 133 against 180, 2048 x 2048: 253 against 268,
-// and 402 with 64 throughout.)
+// and reading 32 columns of partials.  (200 x 333: 78 us against 124 with 256
+// columns throughout, 512 x 512: 99 against 147, 2048 x 2048: 218 against 236,
+// and 325 with 64 throughout; without splits 900 x 900 takes 156 against 133.)
 constexpr int64_t kOrthoPairs = kSms / 2;
-constexpr int64_t kOrthoBlockCycles[3] = {530, 430, 340};  // 256, 128, 64 columns
-constexpr int64_t kOrthoChunkCycles = 2200;
-constexpr int64_t kOrthoSplitCycles = 3000, kOrthoWriteCycles = 300, kOrthoReadCycles = 350;
+constexpr int64_t kOrthoBlockCycles[3] = {510, 380, 280};  // 256, 128, 64 columns
+constexpr int64_t kOrthoChunkCycles = 1500;
+constexpr int64_t kOrthoSplitCycles = 2500, kOrthoWriteCycles = 300, kOrthoReadCycles = 350;
 constexpr int64_t kOrthoLeast = 4;  // blocks that a part keeps
 constexpr int64_t kOrthoClusterPairs = 8;      // CTA pairs of the largest cluster
-constexpr int64_t kOrthoGridBarrier = 2500;    // what the grid's barrier takes more than a cluster's
+constexpr int64_t kOrthoGridBarrier = 600;    // what the grid's barrier takes more than a cluster's
 static_assert(kOrthoPairs <= puro::kSplitTiles, "counters for every split tile");
 
 struct OrthoPlan {
@@ -1298,7 +1298,7 @@ OrthoPlan ortho_plan_for(int64_t n, int64_t k, int64_t pairs) {
 
 // On the whole device, or, where that is estimated to be faster, in one cluster
 // (plan.pairs is then the cluster's, a power of two).
-// (200 x 333: 101 us in one cluster, 123 on the device.)
+// (200 x 333: 78 us in one cluster, 86 on the device; 512 x 512: 119 and 99.)
 OrthoPlan ortho_plan(int64_t n, int64_t k) {
   const OrthoPlan device = ortho_plan_for(n, k, kOrthoPairs);
   OrthoPlan cluster = ortho_plan_for(n, k, kOrthoClusterPairs);
@@ -1311,7 +1311,9 @@ OrthoPlan ortho_plan(int64_t n, int64_t k) {
 }
 
 // Where the workspace of an n x k problem keeps its matrices, in bytes, each
-// from a multiple of 256 on.
+// from a multiple of 256 on.  Rows start on multiples of 128 bytes: the 128-byte
+// rows that TMA reads would else each touch two lines of L2 (900 x 900: 133 us
+// against 156).
 struct OrthoLayout {
   int64_t ld_x, ld_m;
   int64_t x[2][2], o, r, diag, diag_r, part, counters, partial;
@@ -1321,8 +1323,8 @@ struct OrthoLayout {
 OrthoLayout ortho_layout(int64_t n, int64_t k, const OrthoPlan& plan) {
   OrthoLayout l{};
   const int64_t m = n < k ? n : k;
-  l.ld_x = (k + 7) / 8 * 8;
-  l.ld_m = (m + 7) / 8 * 8;
+  l.ld_x = (k + 63) / 64 * 64;
+  l.ld_m = (m + 63) / 64 * 64;
   auto take = [&](int64_t bytes) {
     const int64_t at = l.bytes;
     l.bytes += (bytes + 255) / 256 * 256;
