@@ -120,7 +120,8 @@ struct OrthoCfg {
   static constexpr uint32_t kOffBar = kOffEpi + kEpiBytes;
   static constexpr uint32_t kNumBars = 2 * kStages + 5 + 4 + kBufs * kEpiWarps;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
+  static constexpr uint32_t kOffDiag = (kOffMisc + 16 + 127) / 128 * 128;  // a diagonal at each warp's 32 columns
+  static constexpr uint32_t kSmemBytes = kOffDiag + kEpiWarps * 128 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kTmemCols = 512;          // two accumulators
 };
@@ -404,6 +405,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
   const bool last = EPI == kOrthoUpdate && step == p.steps - 1;
   uint8_t* bufs = sm.base + C::kOffEpi + (warp - 2) * C::kBufs * C::kBuf;
   uint64_t* src_bar = sm.src + (warp - 2) * C::kBufs;
+  float* cols_diag = reinterpret_cast<float*>(sm.base + C::kOffDiag) + (warp - 2) * 32;
   const int sw = (lane >> 1) & 3;  // this lane's row's swizzle
   const float* diag = EPI == kOrthoPoly ? p.diag : p.diag_r;
   for (int32_t u = cluster_id; u < s.units; u += clusters, ++st.it) {
@@ -481,7 +483,11 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
       const int32_t col0 = t.x0 + c * 32;
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_base + c * 32, r);
-      const float dc_lane = d_next;
+      if (kCols) {
+        // (32 shuffles instead: 4096 x 1024 in 170 us against 166)
+        cols_diag[lane] = d_next;
+        __syncwarp();
+      }
       d_next = load_diag(c + dc);
       if (EPI == kOrthoGram) {
         if (lane == 0) bulk_wait_group_read<C::kBufs - 1>();
@@ -544,12 +550,18 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
           const uint4 h4 = *reinterpret_cast<const uint4*>(my_h + ((q ^ sw) << 4));
           const uint4 l4 = EPI == kOrthoUpdate ? *reinterpret_cast<const uint4*>(my_l + ((q ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
           const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
+          float dv[8] = {};
+          if (kCols) {
+            const float4 d0 = *reinterpret_cast<const float4*>(cols_diag + 8 * q);
+            const float4 d1 = *reinterpret_cast<const float4*>(cols_diag + 8 * q + 4);
+            dv[0] = d0.x, dv[1] = d0.y, dv[2] = d0.z, dv[3] = d0.w;
+            dv[4] = d1.x, dv[5] = d1.y, dv[6] = d1.z, dv[7] = d1.w;
+          }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const int e = 8 * q + 2 * w;
             const float2 h = half_unpack(hw[w]);
-            const float d0 = kCols ? __shfl_sync(0xFFFFFFFFu, dc_lane, e) : 0.f;
-            const float d1 = kCols ? __shfl_sync(0xFFFFFFFFu, dc_lane, e + 1) : 0.f;
+            const float d0 = dv[2 * w], d1 = dv[2 * w + 1];
             if (EPI == kOrthoPoly) {
               // R = c (O O + O (D_i + D_j)) + b O off the diagonal
               v[e] = fmaf(v[e], raw_scale * kRScale, h.x * (kRScale / kMScale) * fmaf(p.c, dr + d0, p.b));
