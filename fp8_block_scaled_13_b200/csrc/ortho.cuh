@@ -528,22 +528,20 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
         if (on_diag) {
           float d = 0.f;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e == lane) {
-              d = v[e];
-              v[e] = 0.f;
-            }
+          for (int e = 0; e < 32; ++e) {
+            d = e == lane ? v[e] : d;
+            v[e] = e == lane ? 0.f : v[e];
+          }
           if (row < s.rows_a) p.diag[row] = d * (1.f / kMScale);
         }
       } else {
         const float raw_scale = p.c / (kMScale * kMScale);
         if (EPI == kOrthoPoly && on_diag) {
-          float d_new = 0.f;
+          float own = 0.f;
           // on the diagonal, D' = c ((O O)_ii + D_i^2) + b D_i
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e == lane) d_new = fmaf(v[e], raw_scale, dr * fmaf(p.c, dr, p.b));
-          if (row < s.rows_a) p.diag_r[row] = d_new;
+          for (int e = 0; e < 32; ++e) own = e == lane ? v[e] : own;
+          if (row < s.rows_a) p.diag_r[row] = fmaf(own, raw_scale, dr * fmaf(p.c, dr, p.b));
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -575,8 +573,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
         }
         if (EPI == kOrthoPoly && on_diag) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e == lane) v[e] = 0.f;
+          for (int e = 0; e < 32; ++e) v[e] = e == lane ? 0.f : v[e];
         }
       }
       if (last) {
