@@ -57,6 +57,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "quant.cuh"
 
 namespace puro {
 
@@ -440,6 +441,11 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
       return kCols && c < chunks && x < s.rows_b ? __ldcg(diag + x) : 0.f;
     };
     float d_next = load_diag(c0);
+    // (ready before the products are: parameters and the diagonal are a miss away)
+    float raw_scale = p.c / (kMScale * kMScale), c_r = p.c * (kRScale / kMScale);
+    float base_r = EPI == kOrthoPoly ? fmaf(p.c, dr, p.b) * (kRScale / kMScale) : p.a + dr;
+    float d_own = dr * fmaf(p.c, dr, p.b);
+    if (EPI != kOrthoGram) asm volatile("" : "+f"(raw_scale), "+f"(c_r), "+f"(base_r), "+f"(d_own));
     if (!mbar_wait_warp(&sm.accf[acc], (st.it >> 1) & 1, sm.abort_flag)) return false;
     tc_fence_after();
     const uint32_t t_base = tmem + ((uint32_t)(sp * 32) << 16) + acc * 256;
@@ -535,40 +541,44 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
           if (row < s.rows_a) p.diag[row] = d * (1.f / kMScale);
         }
       } else {
-        const float raw_scale = p.c / (kMScale * kMScale);
         if (EPI == kOrthoPoly && on_diag) {
           float own = 0.f;
           // on the diagonal, D' = c ((O O)_ii + D_i^2) + b D_i
 #pragma unroll
           for (int e = 0; e < 32; ++e) own = e == lane ? v[e] : own;
-          if (row < s.rows_a) p.diag_r[row] = fmaf(own, raw_scale, dr * fmaf(p.c, dr, p.b));
+          if (row < s.rows_a) p.diag_r[row] = fmaf(own, raw_scale, d_own);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint4 h4 = *reinterpret_cast<const uint4*>(my_h + ((q ^ sw) << 4));
           const uint4 l4 = EPI == kOrthoUpdate ? *reinterpret_cast<const uint4*>(my_l + ((q ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
           const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
-          float dv[8] = {};
+          f2 dv[4] = {};
           if (kCols) {
             const float4 d0 = *reinterpret_cast<const float4*>(cols_diag + 8 * q);
             const float4 d1 = *reinterpret_cast<const float4*>(cols_diag + 8 * q + 4);
-            dv[0] = d0.x, dv[1] = d0.y, dv[2] = d0.z, dv[3] = d0.w;
-            dv[4] = d1.x, dv[5] = d1.y, dv[6] = d1.z, dv[7] = d1.w;
+            dv[0] = f2_of(d0.x, d0.y);
+            dv[1] = f2_of(d0.z, d0.w);
+            dv[2] = f2_of(d1.x, d1.y);
+            dv[3] = f2_of(d1.z, d1.w);
           }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const int e = 8 * q + 2 * w;
             const float2 h = half_unpack(hw[w]);
-            const float d0 = dv[2 * w], d1 = dv[2 * w + 1];
+            const f2 raw = f2_of(v[e], v[e + 1]);
+            f2 x;
             if (EPI == kOrthoPoly) {
-              // R = c (O O + O (D_i + D_j)) + b O off the diagonal
-              v[e] = fmaf(v[e], raw_scale * kRScale, h.x * (kRScale / kMScale) * fmaf(p.c, dr + d0, p.b));
-              v[e + 1] = fmaf(v[e + 1], raw_scale * kRScale, h.y * (kRScale / kMScale) * fmaf(p.c, dr + d1, p.b));
+              // R = c (O O + O (D_i + D_j)) + b O off the diagonal: O (c D_j + (c D_i + b)) + c O O
+              x = fma2(raw, f2_both(raw_scale * kRScale), mul2(f2_of(h.x, h.y), fma2(f2_both(c_r), dv[w], f2_both(base_r))));
             } else {
               const float2 l = half_unpack(lw[w]);
-              v[e] = fmaf(p.a + dr + d0, h.x + l.x, v[e] * (1.f / kRScale));
-              v[e + 1] = fmaf(p.a + dr + d1, h.y + l.y, v[e + 1] * (1.f / kRScale));
+              const f2 k = kCols ? fma2(dv[w], f2_both(1.f), f2_both(base_r)) : f2_both(base_r);
+              x = fma2(k, fma2(f2_of(l.x, l.y), f2_both(1.f), f2_of(h.x, h.y)), mul2(raw, f2_both(1.f / kRScale)));
             }
+            const float2 xs = f2_get(x);
+            v[e] = xs.x;
+            v[e + 1] = xs.y;
           }
         }
         if (EPI == kOrthoPoly && on_diag) {
@@ -608,7 +618,8 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
             hi[e] = half_pair(v[i], v[i + 1]);
             if (EPI == kOrthoUpdate) {
               const float2 h = half_unpack(hi[e]);
-              lo[e] = half_pair(v[i] - h.x, v[i + 1] - h.y);
+              const float2 d = f2_get(fma2(f2_of(h.x, h.y), f2_both(-1.f), f2_of(v[i], v[i + 1])));
+              lo[e] = half_pair(d.x, d.y);
             } else if (mirror) {
               // the transposed tile beside it: rows i and i + 1, column lane
               uint8_t* d = buf_l + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2;
