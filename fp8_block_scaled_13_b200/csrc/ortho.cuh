@@ -514,7 +514,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
       // the other parts, in an order that depends on the chunk alone (its owner)
-#pragma unroll 1
+#pragma unroll 2
       for (int32_t k = 1; k < t.parts; ++k) {
         const int32_t other = t.part + k < t.parts ? k : k - t.parts;
         const float4* d = part + (int64_t)other * kPartial + (((int)rank * 8 + c) * 4 + sp) * 256 + lane;
