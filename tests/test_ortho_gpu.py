@@ -142,6 +142,22 @@ def test_size_of_the_gradient(fp8):
     for shape in ((0, 5), (5, 0)):
         assert fp8.orthogonalize(torch.empty(shape, device="cuda")).shape == shape
 
+def test_mixed_sizes_on_several_streams(fp8):
+    # the small kernel, one cluster and the cooperative grid side by side: the same bits as one at a time
+    gs = [_gradient(n, k, i, torch.float32) for i, (n, k) in
+          enumerate([(200, 333), (512, 512), (1024, 700), (100, 90), (900, 900), (333, 200)])]
+    want = [fp8.orthogonalize(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(10):
+        for i, g in enumerate(gs):
+            with torch.cuda.stream(streams[(i + turn) % 3]):
+                got.append((i, fp8.orthogonalize(g)))
+    torch.cuda.synchronize()
+    assert fp8.device_status() == 0
+    assert all(torch.equal(out, want[i]) for i, out in got)
+
 
 @pytest.mark.parametrize("n,k", [(600, 1100), (8, 2000), (150, 200)])
 def test_streams_workspaces_and_graphs(fp8, n, k):
