@@ -820,7 +820,8 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
                                                 step == p.steps - 1 ? &m.out : &m.ex[cur ^ 1][0], &m.ex[cur ^ 1][1],
                                                 tmem, cluster_id, clusters, rank, step, st);
       if (i == products - 1 || (!ok && !p.one_cluster)) break;
-      // this warp's results are in memory
+      // this warp's results are in memory (the wait makes its bulk stores visible to
+      // this thread; the fence that orders them before TMA loads is the readers')
       if (lane == 0) bulk_wait_group<0>();
       __syncwarp();
       if (p.one_cluster) {
