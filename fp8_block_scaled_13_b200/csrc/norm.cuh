@@ -3,12 +3,16 @@
 //
 // Forward, for each token (row of D columns):
 //   hh = h * r1,  r1 = rsqrt(mean(h^2) + eps)      (hh = h without a norm after the block)
-//   y  = bf16(x + scale * gate * hh * w_post)      (y = x without a block output)
+//   y  = bf16(x + scale * ((hh * w_post) * gate))  (y = x without a block output)
 //   n  = bf16(y * r2 * w_pre),  r2 = rsqrt(mean(y^2) + eps)
 // n leaves as E4M3 codes with one scale per 1x128 group, row-wise, transposed
 // or both, exactly as the activation quantizer encodes a BF16 tensor; or as
 // BF16.  r2 is taken from the stored (BF16) y, so that the backward pass and a
-// recomputation from y see the same numbers.
+// recomputation from y see the same numbers.  That makes r2 follow y's rounding:
+// in a strong channel (|y| of 32 or more in a row of 2048 with a mean square of
+// 3) a y that rounds the other way moves r2 by 1e-3.  So y is formed in just
+// this order, each operation rounded to FP32 by itself as separate operations
+// on tensors are: nothing is multiplied ahead and nothing fused.
 //
 // Backward, with t = dn * w_pre, nh = y * r2, e = scale * gate * w_post:
 //   dY = dy + r2 * (t - nh * mean(t nh))     -> dx = bf16(dY)
@@ -67,6 +71,7 @@ struct NormParams {
   int64_t ld_gate;             // kGateFull
   int32_t w_f32, gate_f32, gate_kind;
   int32_t wide;                // w_pre, w_post and a channel gate start on 16-byte boundaries
+  int32_t scale_pow2;          // forward: scale is a power of two
   uint32_t* ctr;               // a tile counter to set to zero for the pass after this one, or null
   float scale, eps;
   // forward
@@ -250,26 +255,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1) n
   fetch(0);
   fetch(B);
 
-  f2 w[4], e[4];
+  f2 w[4], wp[4], gc[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = 0;
-    e[i] = f2_both(p.scale);
-  }
+  for (int i = 0; i < 4; ++i) w[i] = wp[i] = gc[i] = 0;
   const bool emits = p.out.bf || p.out.q;
   if (active) {
-    f2 v[4];
     if (emits) load_param8(p.w_pre, p.w_f32, p.wide, col, w);
-    if (p.w_post) {
-      load_param8(p.w_post, p.w_f32, p.wide, col, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = mul2(e[i], v[i]);
-    }
-    if (p.gate_kind == kGateChannel) {
-      load_param8(p.gate, p.gate_f32, p.wide, col, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = mul2(e[i], v[i]);
-    }
+    if (p.w_post) load_param8(p.w_post, p.w_f32, p.wide, col, wp);
+    if (p.gate_kind == kGateChannel) load_param8(p.gate, p.gate_f32, p.wide, col, gc);
   }
   int buf = 0;
 #pragma unroll 1
@@ -286,7 +279,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1) n
         const uint8_t* s = src + k * tensors * pitch;
         yv[k] = lds_v4(s);
         hv[k] = lds_v4(s + pitch);
-        f[k] = 1.f;
       }
       if (p.w_post) {
 #pragma unroll
@@ -307,18 +299,36 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1) n
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         const int64_t r = row0 + rb + k;
-        if (p.gate_kind == kGateToken && rb + k < nrows) f[k] *= load_param(p.gate, p.gate_f32, r);
         f2 x[4], h[4];
         unpack8(yv[k], x);
         unpack8(hv[k], h);
-        if (p.gate_kind == kGateFull) {
+        if (p.w_post) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = mul2(mul2(h[i], f2_both(f[k])), wp[i]);
+        }
+        if (p.gate_kind == kGateToken) {
+          const f2 g = f2_both(rb + k < nrows ? load_param(p.gate, p.gate_f32, r) : 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = mul2(h[i], g);
+        } else if (p.gate_kind == kGateChannel) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = mul2(h[i], gc[i]);
+        } else if (p.gate_kind == kGateFull) {
           f2 g[4];
           unpack8(lds_v4(src + (k * tensors + 2) * pitch), g);
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = mul2(h[i], g[i]);
         }
+        // (a scale that is a power of two multiplies exactly, so that the fused form
+        // rounds as the two operations do: 32768 x 2048 with a gate per token in 133
+        // us against 139)
+        if (p.scale_pow2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fma2(mul2(h[i], f2_both(f[k])), e[i], x[i]);
+          for (int i = 0; i < 4; ++i) x[i] = fma2(h[i], f2_both(p.scale), x[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = add2(x[i], mul2(h[i], f2_both(p.scale)));
+        }
         yv[k] = pack8(x);
         if (active && rb + k < nrows) *reinterpret_cast<uint4*>(p.y + r * p.ld_y + col) = yv[k];
       }

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <functional>
@@ -1076,6 +1077,8 @@ int puro_fp8_residual_norm(const void* x, int64_t ld_x, const void* h, int64_t l
   p.h = static_cast<const __nv_bfloat16*>(h);
   p.ld_h = ld_h;
   p.eps = eps;
+  int exponent;
+  p.scale_pow2 = std::fabs(std::frexp(scale, &exponent)) == 0.5f;
   p.y = static_cast<__nv_bfloat16*>(y);
   p.ld_y = ld_y;
   p.rstd = rstd;

@@ -299,9 +299,9 @@ PURO_API int puro_fp8_gemm_dgrad_wgrad(const void* qdy, int64_t ld_qdy, const vo
  * (The pages keep the hidden and residual flow and the norms in BF16 around
  * E4M3 linear layers: paperlayer.ai Appendix C.)
  *   hh = h * r1[token],  r1 = rsqrt(mean(h^2) + eps)  (w_post NULL: hh = h)
- *   y  = bf16(x + scale * gate * hh * w_post)         (h NULL: y is x)
+ *   y  = bf16(x + scale * ((hh * w_post) * gate))     (h NULL: y is x)
  *   n  = bf16(y * r2[token] * w_pre),  r2 = rsqrt(mean(y^2) + eps), of the stored y
- * with FP32 sums and factors.  n leaves as codes and scales exactly as
+ * with FP32 sums and factors; y's operations are each rounded to FP32, in this order.  n leaves as codes and scales exactly as
  * puro_fp8_quant_act makes them of that BF16 tensor (layout PURO_ROWWISE,
  * PURO_COLWISE or PURO_BOTH; q, s, qt, st as there), or as itself (PURO_BF16: n).
  * x, h      : BF16 [rows, cols], row strides ld_x, ld_h; h NULL: no block output,
