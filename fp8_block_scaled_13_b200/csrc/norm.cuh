@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_backward_kerne
 
 // Column gradients from the CTAs' partial sums [parts][2][cols], in a fixed
 // order: a block takes 32 columns of one of the two sums, its 16 warps every
-// sixteenth partial.
+// sixteenth partial.  Added in 64 bits and rounded once, so that the error does
+// not grow with the rows (in FP32, 2^20 rows alike were off by 2^-15).
 struct NormColumnParams {
   const float* part;
   int64_t parts;
@@ -585,7 +586,7 @@ struct NormColumnParams {
 };
 
 __global__ void __launch_bounds__(512) norm_column_kernel(const NormColumnParams p) {
-  __shared__ float sm[16][32];
+  __shared__ double sm[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t c = blockIdx.x * 32 + lane;  // cols is a multiple of 128
   // early: the quantizer runs between the row pass and this one.  Its CTAs let
@@ -594,16 +595,17 @@ __global__ void __launch_bounds__(512) norm_column_kernel(const NormColumnParams
   // so that whatever waits for this kernel has waited for both.
   if (!p.early) pdl_wait();
   pdl_trigger();
-  float a = 0.f;
+  double sum = 0.;
   const float* src = p.part + (int64_t)blockIdx.y * p.cols + c;
 #pragma unroll 8
-  for (int64_t i = warp; i < p.parts; i += 16) a += __ldcg(src + i * 2 * p.cols);
-  sm[warp][lane] = a;
+  for (int64_t i = warp; i < p.parts; i += 16) sum += __ldcg(src + i * 2 * p.cols);
+  sm[warp][lane] = sum;
   __syncthreads();
   if (p.early) pdl_wait();
   if (warp) return;
 #pragma unroll
-  for (int k = 1; k < 16; ++k) a += sm[k][lane];
+  for (int k = 1; k < 16; ++k) sum += sm[k][lane];
+  const float a = (float)sum;
   // (explicit adds: fused into the product before them, they would round
   // differently from the call that overwrites)
   const bool add = p.accumulate != 0;
