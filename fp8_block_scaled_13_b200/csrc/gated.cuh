@@ -160,10 +160,22 @@ __device__ __forceinline__ void emit_tile(const uint4 (&v)[8], const CodeOut& o,
   }
 }
 
-// sigmoid(g) of two values; exp(-g) = inf for very negative g gives 0.
+// sigmoid(g) = 1 / (1 + exp(-g)) = 2^-22 / (2^-22 + 2^(-g log2(e) - 22)).  The
+// scaled denominator stays below 2^126 down to g = -102, past which the sigmoid
+// is below FP32's subnormal range (-inf gives 0); unscaled it leaves the range of
+// a reciprocal at g = -87.3, and products with a large u lost what is left there.
+// The exponent is rounded to 2^-24 of itself, so the sigmoid is off by 2^-19 +
+// |g| 2^-22 of itself, against the half step of 2^-9 when a result is rounded to
+// BF16.  (32768 x 6144: 204 us; 201 unscaled; 212 with exp(-|g|) and a choice of
+// the numerator; 239 with expf.)
+__device__ __forceinline__ float sigmoid1(float g) {
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.4426950408889634f, -22.f)));
+  return __fdividef(0x1p-22f, e + 0x1p-22f);
+}
 __device__ __forceinline__ f2 sigmoid2(f2 g) {
   const float2 v = f2_get(g);
-  return f2_of(__fdividef(1.f, 1.f + __expf(-v.x)), __fdividef(1.f, 1.f + __expf(-v.y)));
+  return f2_of(sigmoid1(v.x), sigmoid1(v.y));
 }
 
 template <bool BWD, bool ROW, bool COL, bool BF>
@@ -226,9 +238,10 @@ __global__ void __launch_bounds__(256, 2)
         unpack8(lds_v4(src + 2 * kQTileBytes + k * 256), d);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f2 s = sigmoid2(g[e]), ds = mul2(d[e], s), one = f2_both(1.f);
-          d[e] = mul2(ds, g[e]);                                                           // du
-          g[e] = mul2(mul2(ds, u[e]), fma2(g[e], fma2(s, f2_both(-1.f), one), one));       // dg
+          // (the small factor s last: a product with it first could leave FP32's range)
+          const f2 s = sigmoid2(g[e]), one = f2_both(1.f), du = mul2(mul2(d[e], g[e]), s);
+          g[e] = mul2(mul2(mul2(d[e], u[e]), s), fma2(g[e], fma2(s, f2_both(-1.f), one), one));  // dg
+          d[e] = du;
         }
         w[BWD ? k : 0] = pack8(d);
       }
