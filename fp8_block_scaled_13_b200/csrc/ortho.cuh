@@ -14,14 +14,29 @@
 // off the diagonal: with M = D + O and R = D' + O' (D, D' diagonal, in FP32)
 //   M^2 = O O + D O + O D + D^2,      a X + R X = (a + D') X + O' X,
 // the tensor cores compute X X^T, O O and O' X from FP16 operands, one product
-// each, and the epilogues add the rest in FP32 from the exact parts.  What the
-// operands lose is random and averaged over the long sums, and the large,
-// coherent parts -- the diagonals, and X itself -- are not rounded at all: off by
-// 3e-4 to 8e-4 for Gaussian, low-rank, power-law and geometric spectra.  (Two
-// BF16 terms per operand and three products each were as exact and took twice
-// as long: 2168 us against 1133 for 12288 x 2048.)  A short sum averages
-// less, so X X^T over up to kOrthoExactK takes three products, hi hi + hi lo +
-// lo hi, where launches and not products are the time anyway.
+// each, and the epilogues add the rest in FP32.  X itself is exact to 22 bits, the
+// diagonals come from FP32 sums (of operands that are rounded where X X^T is long,
+// see below).  Two things keep what the operands lose small for every gradient:
+//  - It is rounded at random (up or down by how near the value lies), so that
+//    over the long sums it averages out.  Rounded to nearest, equal entries all
+//    err alike: all-equal gradients of 160 x 1342 and 640 x 5377 were 1.0e-2 and
+//    1.1e-2 off, where they now are off by the rounding of the result alone.
+//  - What X loses must not leave the span of X's rows and columns, since a
+//    direction that X lacks is lifted by a = 3.4 in each later step.  O' (X - hi)
+//    does leave it, by what the diagonal is missing; R (X - hi) does not.  So D'
+//    multiplies hi alone, and all of X only in the last two steps, where
+//    nothing lifts it any more and what the hi term loses would count at the
+//    large directions.  (D' X throughout: a rank-1 gradient was 2e-3 to 3e-3 off at
+//    sides of 130 to 300, and after ten steps by 0.2 to 0.9 of its size.)
+// Off by 3e-4 to 1.1e-3 in 5 steps, before out is rounded, at sides above 128, for
+// Gaussian, low-rank, all-equal, sign, block and row-repeating gradients (to
+// nearest, the Gaussian ones 3e-4 to 6e-4, now 5e-4 to 9e-4).  More steps lift
+// whatever is there: each takes what X's 22 bits and FP32 sums leave in a
+// direction that G lacks up by a, to 2e-2 to 7e-2 in ten steps.  (Two BF16 terms
+// per operand and three products each took twice as long: 2168 us against 1133
+// for 12288 x 2048.)  A short sum averages less, so X X^T over up to kOrthoExactK
+// takes three products, hi hi + hi lo + lo hi, where launches and not products are
+// the time anyway.
 // Powers of two keep FP16 in range: X is stored times 2^10, M times 2^13, R
 // times 2^12, which holds while |X| < 64, |M| < 8 and |R| < 16 off the
 // diagonal; the iteration keeps singular values near 1.
@@ -65,6 +80,7 @@ enum OrthoProduct : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2 };
 
 constexpr int kOrthoNormBlocks = 592;  // most CTAs of the passes over G, one partial sum each
 constexpr int64_t kOrthoExactK = 1024; // longest X X^T sum that takes three products
+constexpr int kOrthoLate = 2;           // last steps in which all of X meets the diagonal of R
 constexpr float kXScale = 1024.f, kMScale = 8192.f, kRScale = 4096.f;
 constexpr int kOrthoMaxSplit = 8;
 
@@ -192,6 +208,28 @@ __device__ __forceinline__ OrthoUnit ortho_unit(const OrthoShape& s, int32_t u) 
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// The same with each value rounded up or down at random, by how near it lies, on
+// bits 0..12 (lo) and 16..28 (hi) of `bits`.
+__device__ __forceinline__ uint32_t half_pair_random(float lo, float hi, uint32_t bits) {
+  uint32_t d;
+  asm("cvt.rs.f16x2.f32 %0, %1, %2, %3;" : "=r"(d) : "f"(hi), "f"(lo), "r"(bits));
+  return d;
+}
+
+// Bits for the roundings of a row's pairs of columns, from column `col` on, in
+// one product: for the pair n, first + n * step.  They follow from the place
+// alone, so that a result repeats.  (The constants are the odd ones among the
+// binary fractions of the square roots of 2, 3, 11, 17 and 19.)
+struct RoundBits {
+  uint32_t first, step;
+};
+__device__ __forceinline__ RoundBits round_bits(int32_t row, int32_t col, int32_t product) {
+  uint32_t h = (uint32_t)row * 0x6A09E667u + (uint32_t)col * 0xBB67AE85u + (uint32_t)product * 0x510E527Fu;
+  h = (h ^ (h >> 15)) * 0x1F83D9ABu;
+  h = (h ^ (h >> 14)) * 0x5BE0CD19u;
+  return {h ^ (h >> 16), h * 0x6A09E667u + 0xBB67AE85u};
 }
 
 __device__ __forceinline__ float2 half_unpack(uint32_t w) {
@@ -445,6 +483,8 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
     float raw_scale = p.c / (kMScale * kMScale), c_r = p.c * (kRScale / kMScale);
     float base_r = EPI == kOrthoPoly ? fmaf(p.c, dr, p.b) * (kRScale / kMScale) : p.a + dr;
     float d_own = dr * fmaf(p.c, dr, p.b);
+    // the update's factors of X's terms: a + D' for hi, for lo a, and a + D' late
+    const float late = step + kOrthoLate >= p.steps ? 1.f : 0.f, k_low = fmaf(late, dr, p.a);
     if (EPI != kOrthoGram) asm volatile("" : "+f"(raw_scale), "+f"(c_r), "+f"(base_r), "+f"(d_own));
     if (!mbar_wait_warp(&sm.accf[acc], (st.it >> 1) & 1, sm.abort_flag)) return false;
     tc_fence_after();
@@ -574,7 +614,8 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
             } else {
               const float2 l = half_unpack(lw[w]);
               const f2 k = kCols ? fma2(dv[w], f2_both(1.f), f2_both(base_r)) : f2_both(base_r);
-              x = fma2(k, fma2(f2_of(l.x, l.y), f2_both(1.f), f2_of(h.x, h.y)), mul2(raw, f2_both(1.f / kRScale)));
+              const f2 k_lo = kCols ? fma2(dv[w], f2_both(late), f2_both(p.a)) : f2_both(k_low);
+              x = fma2(k, f2_of(h.x, h.y), fma2(k_lo, f2_of(l.x, l.y), mul2(raw, f2_both(1.f / kRScale))));
             }
             const float2 xs = f2_get(x);
             v[e] = xs.x;
@@ -609,13 +650,15 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
           continue;
         }
       } else {
+        RoundBits rb = round_bits(row, col0, 3 * step + EPI);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 8 * q + 2 * e;
-            hi[e] = half_pair(v[i], v[i + 1]);
+            hi[e] = half_pair_random(v[i], v[i + 1], rb.first);
+            rb.first += rb.step;
             if (EPI == kOrthoUpdate) {
               const float2 h = half_unpack(hi[e]);
               const float2 d = f2_get(fma2(f2_of(h.x, h.y), f2_both(-1.f), f2_of(v[i], v[i + 1])));
@@ -940,10 +983,11 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const OrthoSplitParams
     float v[8];
     load_g8<F32, VEC>(p, r, (int32_t)c, v);
     uint32_t h[4], l[4];
+    const RoundBits rb = round_bits((int32_t)r, (int32_t)c, -1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float x = v[2 * e] * scale, y = v[2 * e + 1] * scale;
-      h[e] = half_pair(x, y);
+      h[e] = half_pair_random(x, y, rb.first + e * rb.step);
       const float2 f = half_unpack(h[e]);
       l[e] = half_pair(x - f.x, y - f.y);
     }

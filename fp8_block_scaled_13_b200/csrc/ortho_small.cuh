@@ -15,10 +15,11 @@
 //             M = sum over the cluster, through distributed shared memory: CTA p
 //               adds the rows of its band in a fixed order and hands them to all
 //             S = O O;  R = c (S + O D + D O) + b O          tensor cores, epilogue
-//             X_p <- (a + D') X_p + R X_p                    tensor cores, epilogue
-// (scales, D, D' as in ortho.cuh; only the operands of products are rounded, to
-// 22 bits for X X^T and to 11 for O and R off their diagonals, and X itself is
-// FP32 from step to step).  Every CTA forms the whole of S and R for itself:
+//             X_p <- (a + D') X_p + R X_p (R hi, R lo)       tensor cores, epilogue
+// (scales, D, D' as in ortho.cuh; only the operands of products are rounded, X to
+// 22 bits, O and R off their diagonals at random to 11, and X itself is FP32 from
+// step to step: what the products of few rows lost of X with hi alone left a rank-1
+// gradient 3e-2 off).  Every CTA forms the whole of S and R for itself:
 // that is less than handing them over would take.  Bound by latency.
 #pragma once
 
@@ -89,6 +90,12 @@ __device__ __forceinline__ void st_peer_v4(uint32_t addr, const uint4& v) {
 }
 __device__ __forceinline__ void st_peer_f1(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Eight values as FP16, rounded at random.
+__device__ __forceinline__ uint4 half_row8(const float* v, const RoundBits& b) {
+  return make_uint4(half_pair_random(v[0], v[1], b.first), half_pair_random(v[2], v[3], b.first + b.step),
+                    half_pair_random(v[4], v[5], b.first + 2 * b.step), half_pair_random(v[6], v[7], b.first + 3 * b.step));
 }
 
 // Byte of a 16-byte piece (8 columns from c on) of row r in two [128][64] tiles.
@@ -318,11 +325,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             }
           diag[row] = d * (1.f / kMScale);
         }
+        const RoundBits rb = round_bits(row, c, 3 * step);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<uint4*>(tile_o + small_piece(row, c + 8 * q)) =
-              make_uint4(half_pair(v[8 * q], v[8 * q + 1]), half_pair(v[8 * q + 2], v[8 * q + 3]),
-                         half_pair(v[8 * q + 4], v[8 * q + 5]), half_pair(v[8 * q + 6], v[8 * q + 7]));
+              half_row8(v + 8 * q, {rb.first + 4 * q * rb.step, rb.step});
       }
       hand_over();
     } else {
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
               v[e] = 0.f;
             }
         }
-        const uint4 o = make_uint4(half_pair(v[0], v[1]), half_pair(v[2], v[3]), half_pair(v[4], v[5]), half_pair(v[6], v[7]));
+        const uint4 o = half_row8(v, round_bits(r, c, 3 * step));
         const uint32_t to = smem_u32(tile_o + small_piece(r, c)), to_d = smem_u32(diag + r);
         for (uint32_t q = 0; q < peers; ++q) {
           st_peer_v4(cluster_peer(to, q), o);
@@ -399,6 +406,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
       regs_after_wait(r);
       const bool on_diag = (row & ~31) == c;
       const float raw = p.c / (kMScale * kMScale);
+      RoundBits rb = round_bits(row, c, 3 * step + 1);
       float d_new = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -423,21 +431,25 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             d_new = fmaf(s1, raw, dr * fmaf(p.c, dr, p.b));
             v1 = 0.f;
           }
-          o[w] = half_pair(v0, v1);
+          o[w] = half_pair_random(v0, v1, rb.first);
+          rb.first += rb.step;
         }
         *at = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (on_diag) diag_r[row] = d_new;
     }
     hand_over();
-    // ---- R X_p: B is X hi read MN-major, its 64-column tiles 16 KB apart
+    // ---- R X_p: B is X hi, then X lo, read MN-major, its 64-column tiles 16 KB apart
     if (warp == 0) {
       if (elect_one()) {
-        for (int k = 0; k < m16 / 16; ++k) {
-          const uint64_t b = (uint64_t)(((sb + k * 2048) & 0x3FFFFu) >> 4) | ((uint64_t)(16384u >> 4) << 16) |
-                             ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
-          tc_mma_f16_1(tmem + 128, kmajor(C::kOffO, k), b, idesc(128, true), k > 0);
-        }
+        uint32_t accumulate = 0;
+        for (uint32_t term = 0; term < 2 * C::kOffLo; term += C::kOffLo)
+          for (int k = 0; k < m16 / 16; ++k) {
+            const uint64_t b = (uint64_t)(((sb + term + k * 2048) & 0x3FFFFu) >> 4) | ((uint64_t)(16384u >> 4) << 16) |
+                               ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+            tc_mma_f16_1(tmem + 128, kmajor(C::kOffO, k), b, idesc(128, true), accumulate);
+            accumulate = 1;
+          }
         tc_commit_local<1>(bar);
       }
       __syncwarp();

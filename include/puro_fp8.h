@@ -396,7 +396,10 @@ PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
  * out  : BF16 [n, k], any row stride ld_out >= k; must not overlap g.
  * X is held to 22 significant bits (two FP16 terms), the diagonals of M and of
  * b M + c M^2 in FP32, and every product accumulates in FP32; what enters a
- * product is rounded to FP16 off the diagonal, and out to BF16 once.
+ * product is rounded to FP16 off the diagonal, up or down at random by bits that
+ * follow from its place (results repeat), and out to BF16 once.  In 5 steps that
+ * adds 1.1e-3 of the result at most to the rounding of out; every further step
+ * lifts by a what 22 bits leave in directions that G lacks.
  * 1 <= n, k <= 65536 (0: no-op); 1 <= steps <= 64; eps >= 0; coefficients that
  * let a singular value from [0, 1] reach 2 are refused (PURO_ERR_SHAPE).
  * Large gradients take a cooperative launch, which waits until all its CTAs fit
