@@ -1347,18 +1347,35 @@ OrthoLayout ortho_layout(int64_t n, int64_t k, const OrthoPlan& plan) {
 
 // Whether the FP16 form holds the iteration with these coefficients: from
 // singular values in [0, 1], X stays below 2, so that |M| <= 4, and |R| <= 15.
-bool ortho_in_range(int steps, float a, float b, float c) {
-  constexpr int kPoints = 256;
-  float x[kPoints];
-  for (int i = 0; i < kPoints; ++i) x[i] = (float)(i + 1) / kPoints;
-  bool ok = true;
-  for (int s = 0; s < steps && ok; ++s)
-    for (int i = 0; i < kPoints; ++i) {
-      const float q = x[i] * x[i], r = q * (b + c * q);
-      x[i] *= a + r;
-      ok = ok && x[i] > -2.f && x[i] < 2.f && r > -15.f && r < 15.f;
+// A step maps the values in [0, h] onto just [0, max |x p(x)|], and the maximum is
+// at h or where the quintic's slope a + 3 b q + 5 c q^2 (q = x^2) is zero.  (Points
+// of a grid don't do: a chaotic quintic takes the values between them elsewhere.)
+// 2^-9 a step is left for the roundings.
+bool ortho_in_range(int steps, double a, double b, double c) {
+  double h = 1.;
+  for (int s = 0; s < steps; ++s) {
+    h *= 1. + 0x1p-9;
+    const double q_h = h * h, d = 9. * b * b - 20. * c * a;
+    double top = 0., r_top = 0.;
+    auto visit = [&](double q) {  // (a NaN is no place in the interval)
+      if (!(q >= 0. && q <= q_h)) return;
+      const double r = q * (b + c * q);
+      top = std::max(top, std::fabs(std::sqrt(q) * (a + r)));
+      r_top = std::max(r_top, std::fabs(r));
+    };
+    visit(q_h);
+    visit(-b / (2. * c));  // the extreme of r
+    visit(-a / (3. * b));  // a slope without its quadratic term
+    if (d >= 0.) {
+      // the two roots without cancellation: one from the sum of like signs, the other from their product
+      const double t = -(3. * b + std::copysign(std::sqrt(d), b));
+      visit(t / (10. * c));
+      visit(2. * a / t);
     }
-  return ok;
+    if (!(top < 2. && r_top < 15.)) return false;
+    h = top;
+  }
+  return true;
 }
 
 template <bool TALL>
@@ -1479,7 +1496,7 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
   if (g_f32 & ~1) return PURO_ERR_LAYOUT;
   if (n < 0 || k < 0 || n > kOrthoMaxDim || k > kOrthoMaxDim || steps < 1 || steps > kOrthoMaxSteps || !(eps >= 0.f))
     return PURO_ERR_SHAPE;
-  if (!ortho_in_range(steps, a, b, c)) return PURO_ERR_SHAPE;
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !ortho_in_range(steps, a, b, c)) return PURO_ERR_SHAPE;
   if (n == 0 || k == 0) return PURO_OK;
   if (!g || !out || !workspace) return PURO_ERR_NULL;
   if (!aligned_to(g, g_f32 ? 4 : 2) || !aligned_to(out, 2) || !aligned_to(workspace, 256)) return PURO_ERR_ALIGN;
