@@ -13,7 +13,7 @@ _API = ("quant_act", "quant_weight", "blocked_scale_bytes", "gemm_fprop", "gemm_
         "gemm_dgrad_wgrad", "device_status", "linear_forward", "linear_backward", "QuantAct",
         "QuantWeight")
 _BLOCK = ("residual_norm", "residual_norm_backward", "swiglu", "swiglu_backward", "ResidualNorm", "ResidualNormGrad")
-_MUON = ("orthogonalize",)
+_MUON = ("orthogonalize", "orthogonalize_workspace_bytes")
 
 
 def __getattr__(name):

@@ -547,10 +547,19 @@ PyObject* orthogonalize(PyObject* const* a, Py_ssize_t n_args) {
   }
   const int64_t need = puro_fp8_orthogonalize_workspace_bytes(n, k);
   at::Tensor ws;
-  if (workspace)
+  if (workspace) {
     need_bytes(workspace, need);
-  else
+    if (reinterpret_cast<uintptr_t>(workspace.ptr()) % 256) value_error("workspace must start on a multiple of 256 bytes");
+    const char *w0 = static_cast<const char*>(workspace.ptr()), *w1 = w0 + need;
+    auto meets = [&](const Arg& a, int64_t ld, int64_t element) {
+      const char* p0 = static_cast<const char*>(a.ptr());
+      return n && k && w0 < p0 + ((n - 1) * ld + k) * element && p0 < w1;
+    };
+    if (meets(g, ld_g, type == at::kFloat ? 4 : 2)) value_error("workspace must not overlap g");
+    if (out && meets(out, ld_out, 2)) value_error("workspace must not overlap out");
+  } else {
     ws = dev.empty({need > 256 ? need : 256}, at::kByte);
+  }
   void* stream = dev.stream();
   const int st = unlocked([&] {
     return puro_fp8_orthogonalize(g.ptr(), ld_g, type == at::kFloat, n, k, steps, ca, cb, cc, eps,

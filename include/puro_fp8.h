@@ -393,7 +393,8 @@ PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
  * g    : [n, k] FP32 (g_f32 = 1, e.g. a main gradient) or BF16 (0), any row
  *        stride ld_g >= k and any alignment of its type; |g| below 1e18 (its
  *        squares are summed in FP32).
- * out  : BF16 [n, k], any row stride ld_out >= k; must not overlap g.
+ * out  : BF16 [n, k], any row stride ld_out >= k; must not overlap g, and the
+ *        workspace neither of them.
  * X is held to 22 significant bits (two FP16 terms), the diagonals of M and of
  * b M + c M^2 in FP32, and every product accumulates in FP32; what enters a
  * product is rounded to FP16 off the diagonal, up or down at random by bits that
