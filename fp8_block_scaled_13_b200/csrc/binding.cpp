@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdarg>
 #include <initializer_list>
 #include <set>
@@ -331,9 +332,11 @@ double number(PyObject* o) {
   return v;
 }
 
-int integer(PyObject* o) {
-  const long v = PyLong_AsLong(o);
+int integer(PyObject* o, const char* name) {
+  int overflow = 0;
+  const long v = PyLong_AsLongAndOverflow(o, &overflow);
   if (v == -1 && PyErr_Occurred()) throw PythonError();
+  if (overflow || v < INT_MIN || v > INT_MAX) value_error("%s is out of range", name);
   return (int)v;
 }
 
@@ -373,7 +376,7 @@ PyObject* residual_norm(PyObject* const* a, Py_ssize_t n) {
   const Arg x(a[0], "x", false), w_pre(a[1], "w_pre", false), h(a[2], "h"), w_post(a[3], "w_post"), gate(a[4], "gate"),
       y(a[8], "y");
   const float scale = (float)number(a[5]), eps = (float)number(a[6]);
-  Result res(a[9], integer(a[7]));
+  Result res(a[9], integer(a[7], "layout"));
   const OnDevice dev("residual_norm", {&x, &w_pre, &h, &w_post, &gate, &y, &res.q, &res.s, &res.qt, &res.st, &res.bf});
   need_any_matrix(x);
   const int64_t rows = x.t->size(0), cols = x.t->size(1);
@@ -419,7 +422,7 @@ PyObject* residual_norm_backward(PyObject* const* a, Py_ssize_t n) {
   const float scale = (float)number(a[9]);
   const int accumulate = PyObject_IsTrue(a[16]);
   if (accumulate < 0) throw PythonError();
-  Result res(a[12], integer(a[10]));
+  Result res(a[12], integer(a[10], "layout"));
   const OnDevice dev("residual_norm_backward",
                      {&dn, &y, &rstd, &w_pre, &h, &dy, &w_post, &rstd_post, &gate, &dx, &dw_pre, &dw_post, &dgate,
                       &res.q, &res.s, &res.qt, &res.st, &res.bf});
@@ -476,7 +479,7 @@ PyObject* residual_norm_backward(PyObject* const* a, Py_ssize_t n) {
 PyObject* swiglu(PyObject* const* a, Py_ssize_t n) {
   need_count(n, 3);
   const Arg gu(a[0], "gu", false);
-  Result res(a[2], integer(a[1]));
+  Result res(a[2], integer(a[1], "layout"));
   const OnDevice dev("swiglu", {&gu, &res.q, &res.s, &res.qt, &res.st, &res.bf});
   need_any_matrix(gu);
   const int64_t rows = gu.t->size(0), f2 = gu.t->size(1);
@@ -494,7 +497,7 @@ PyObject* swiglu(PyObject* const* a, Py_ssize_t n) {
 PyObject* swiglu_backward(PyObject* const* a, Py_ssize_t n) {
   need_count(n, 4);
   const Arg da(a[0], "da", false), gu(a[1], "gu", false);
-  Result res(a[3], integer(a[2]));
+  Result res(a[3], integer(a[2], "layout"));
   const OnDevice dev("swiglu_backward", {&da, &gu, &res.q, &res.s, &res.qt, &res.st, &res.bf});
   need_any_matrix(da);
   const int64_t rows = da.t->size(0), f = da.t->size(1);
@@ -520,7 +523,7 @@ int64_t need_rows(const Arg& a) {
 PyObject* orthogonalize(PyObject* const* a, Py_ssize_t n_args) {
   need_count(n_args, 8);
   const Arg g(a[0], "g", false), out(a[6], "out"), workspace(a[7], "workspace");
-  const int steps = integer(a[1]);
+  const int steps = integer(a[1], "steps");
   const float ca = (float)number(a[2]), cb = (float)number(a[3]), cc = (float)number(a[4]), eps = (float)number(a[5]);
   const OnDevice dev("orthogonalize", {&g, &out, &workspace});
   need_cuda(g);

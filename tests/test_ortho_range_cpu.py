@@ -61,3 +61,12 @@ def test_against_fine_grids():
             assert (status == _lib.PURO_OK) or top > 1.89, (a, b, c, steps)
             taken += status == _lib.PURO_OK
     assert refused > 50 and taken > 20
+
+
+@pytest.mark.parametrize("steps", [2 ** 32 + 5, -2 ** 32 + 5, 2 ** 31, 2 ** 70, -2 ** 70])
+def test_step_counts_beyond_an_int_are_refused(steps):
+    """Cut to 32 bits, the first two are 5."""
+    import torch
+    import fp8_block_scaled_13_b200 as fp8
+    with pytest.raises(ValueError, match="steps"):
+        fp8.orthogonalize(torch.zeros(8, 8), steps=steps)
