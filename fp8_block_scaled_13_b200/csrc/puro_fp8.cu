@@ -1383,7 +1383,7 @@ int launch_ortho(const puro::OrthoMaps& m, const puro::OrthoParams& p, int64_t p
                  cudaStream_t stream) {
   using C = puro::OrthoCfg;
   auto kern = puro::ortho_kernel<TALL>;
-  static std::atomic<int> max_pairs[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices] = {};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1396,17 +1396,21 @@ int launch_ortho(const puro::OrthoMaps& m, const puro::OrthoParams& p, int64_t p
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (max_pairs[dev.index].load(std::memory_order_acquire) == 0) {
-    int n = 0;
+  if (!done[dev.index].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
       cudaGetLastError();
       return PURO_ERR_CUDA;
     }
-    max_pairs[dev.index].store(n, std::memory_order_release);
+    done[dev.index].store(true, std::memory_order_release);
   }
-  if (max_pairs[dev.index].load(std::memory_order_acquire) < pairs) return PURO_ERR_UNSUPPORTED_DEVICE;
+  // (asked for every launch: a context may have only some of the device's SMs)
+  int resident = 0;
+  if (cudaOccupancyMaxActiveClusters(&resident, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return PURO_ERR_CUDA;
+  }
+  if (resident < pairs) return PURO_ERR_UNSUPPORTED_DEVICE;
   cfg.gridDim = dim3(2 * (unsigned)pairs);
   cfg.numAttrs = 2;
   if (p.one_cluster) {
