@@ -2,6 +2,7 @@
 wrappers _binding.so (g++, against torch) in-tree."""
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -17,6 +18,7 @@ DEPS = ["puro_fp8.cu", "common.cuh", "quant.cuh", "gemm.cuh", "norm.cuh", "gated
 HEADER = os.path.join(ROOT, "include", "puro_fp8.h")
 BINDING_PATH = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_TARGET_PATH = os.path.join(HERE, "_binding.target")  # the interpreter and torch that _binding.so is for
 
 
 def nvcc_path() -> str:
@@ -61,15 +63,33 @@ def stale() -> bool:
     return _stale(LIB_PATH, [os.path.join(CSRC, d) for d in DEPS] + [HEADER])
 
 
+def binding_target() -> str:
+    return "%s torch %s\n" % (sysconfig.get_config_var("SOABI"), importlib.metadata.version("torch"))
+
+
+def binding_stale() -> bool:
+    if _stale(BINDING_PATH, [BINDING_SOURCE, HEADER]):
+        return True
+    try:
+        with open(BINDING_TARGET_PATH) as f:
+            return f.read() != binding_target()
+    except OSError:
+        return True
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or stale():
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
         subprocess.run(nvcc_command(tmp, verbose_ptxas), check=True)
         os.replace(tmp, LIB_PATH)
-    if force or _stale(BINDING_PATH, [BINDING_SOURCE, HEADER]):
+    if force or binding_stale():
         tmp = BINDING_PATH + ".tmp%d" % os.getpid()
         subprocess.run(binding_command(tmp), check=True)
         os.replace(tmp, BINDING_PATH)
+        tmp = BINDING_TARGET_PATH + ".tmp%d" % os.getpid()
+        with open(tmp, "w") as f:
+            f.write(binding_target())
+        os.replace(tmp, BINDING_TARGET_PATH)
     return LIB_PATH
 
 
