@@ -17,6 +17,7 @@
 #include <functional>
 #include <mutex>
 #include <queue>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/puro_fp8.h"
@@ -944,16 +945,31 @@ int launch_norm_pass(Kern kern, std::atomic<bool>* done, uint32_t max_smem, cons
                         stream);
 }
 
-template <int MAXT, int ROWS>
-int launch_norm_forward(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
+template <int MAXT, int ROWS, bool POST, int GATE>
+int launch_norm_forward_as(puro::NormParams p, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices] = {};
-  // 16 forward, for an even end (32768 x 2048: 119 us; 125 with 32 rows, 124 with
-  // 8), but 32 where one CTA fills an SM (8192 x 8192: 138 us against 141)
+  // 16 forward, for an even end (32768 x 2048, both norms and a gate per token: 117
+  // us; 124 with 32 rows, 122 with 8), but 32 where one CTA fills an SM (8192 x
+  // 8192: 142 us against 145)
   p.rpc = norm_rpc(p.rows, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1, MAXT == 1024 ? 32 : 16, ROWS);
   const int threads = (p.cols / 8 + 31) / 32 * 32;
-  const int tensors = 1 + (p.h != nullptr) + (p.gate_kind == PURO_GATE_FULL);
-  return launch_norm_pass(puro::norm_forward_kernel<MAXT, ROWS>, done, puro::norm_pass_smem(ROWS, MAXT, 3), p,
+  const int tensors = 1 + (p.h != nullptr) + (GATE == PURO_GATE_FULL);
+  return launch_norm_pass(puro::norm_forward_kernel<MAXT, ROWS, POST, GATE>, done, puro::norm_pass_smem(ROWS, MAXT, 3), p,
                           puro::norm_pass_smem(ROWS, threads, tensors), dev, stream);
+}
+
+template <int MAXT, int ROWS>
+int launch_norm_forward(const puro::NormParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  auto with_gate = [&](auto post) {
+    constexpr bool kPost = decltype(post)::value;
+    switch (p.gate_kind) {
+      case PURO_GATE_TOKEN: return launch_norm_forward_as<MAXT, ROWS, kPost, PURO_GATE_TOKEN>(p, dev, stream);
+      case PURO_GATE_CHANNEL: return launch_norm_forward_as<MAXT, ROWS, kPost, PURO_GATE_CHANNEL>(p, dev, stream);
+      case PURO_GATE_FULL: return launch_norm_forward_as<MAXT, ROWS, kPost, PURO_GATE_FULL>(p, dev, stream);
+      default: return launch_norm_forward_as<MAXT, ROWS, kPost, PURO_GATE_NONE>(p, dev, stream);
+    }
+  };
+  return p.w_post ? with_gate(std::true_type{}) : with_gate(std::false_type{});
 }
 
 template <int MAXT, int ROWS>
