@@ -19,7 +19,7 @@
 // not been launched yet (cluster launch control), so that SMs that stream
 // faster take more tiles without a counter to set up.  (One tile per CTA,
 // loaded into registers, left the memory idle while it was encoded:
-// 32768 x 6144 took 300 us, 16384 x 6144 backward 261 us, against 203 and 174;
+// 32768 x 6144 took 300 us, 16384 x 6144 backward 261 us, against 204 and 178;
 // at the copy rate the bytes alone take 184 and 154.)
 #pragma once
 

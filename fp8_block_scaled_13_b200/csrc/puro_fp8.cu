@@ -916,7 +916,7 @@ int norm_rpc(int64_t rows, int64_t resident, int most, int least) {
   return rpc;
 }
 // 32 backward: each CTA leaves 8 bytes per column for the column pass
-// (32768 x 2048: 233 us with 32 rows, 247 with 16, 241 with 64).
+// (32768 x 2048: 230 us with 32 rows, 243 with 16, 235 with 64).
 int norm_backward_rpc(int64_t rows, int64_t cols) {
   return norm_rpc(rows, cols <= 2048 ? 2 : 1, 32, cols <= 4096 ? 4 : 2);
 }
@@ -1247,9 +1247,9 @@ constexpr int64_t kOrthoMaxDim = 65536;
 // pairs a split along k, that together should take the least time.  In cycles,
 // measured on a B200: a 64-deep block of a tile, by its width; 32 columns of an
 // epilogue, which two sets of warps share; a split tile's hand-over, and writing
-// and reading 32 columns of partials.  (200 x 333: 78 us against 124 with 256
-// columns throughout, 512 x 512: 99 against 147, 2048 x 2048: 218 against 236,
-// and 325 with 64 throughout; without splits 900 x 900 takes 156 against 133.)
+// and reading 32 columns of partials.  (200 x 333: 74 us against 118 with 256
+// columns throughout, 512 x 512: 97 against 146, 2048 x 2048: 219 against 239,
+// and 327 with 64 throughout; without splits 900 x 900 takes 142 against 131.)
 constexpr int64_t kOrthoPairs = kSms / 2;
 constexpr int64_t kOrthoBlockCycles[3] = {510, 380, 280};  // 256, 128, 64 columns
 constexpr int64_t kOrthoChunkCycles = 1500;
@@ -1317,7 +1317,7 @@ OrthoPlan ortho_plan_for(int64_t n, int64_t k, int64_t pairs) {
 
 // On the whole device, or, where that is estimated to be faster, in one cluster
 // (plan.pairs is then the cluster's, a power of two).
-// (200 x 333: 78 us in one cluster, 86 on the device; 512 x 512: 119 and 99.)
+// (200 x 333: 74 us in one cluster, 82 on the device; 512 x 512: 109 and 97.)
 OrthoPlan ortho_plan(int64_t n, int64_t k) {
   const OrthoPlan device = ortho_plan_for(n, k, kOrthoPairs);
   OrthoPlan cluster = ortho_plan_for(n, k, kOrthoClusterPairs);
@@ -1331,8 +1331,8 @@ OrthoPlan ortho_plan(int64_t n, int64_t k) {
 
 // Where the workspace of an n x k problem keeps its matrices, in bytes, each
 // from a multiple of 256 on.  Rows start on multiples of 128 bytes: the 128-byte
-// rows that TMA reads would else each touch two lines of L2 (900 x 900: 133 us
-// against 156).
+// rows that TMA reads would else each touch two lines of L2 (900 x 900: 131 us
+// against 155).
 struct OrthoLayout {
   int64_t ld_x, ld_m;
   int64_t x[2][2], o, r, diag, diag_r, part, counters, partial;
@@ -1445,7 +1445,7 @@ int launch_ortho(const puro::OrthoMaps& m, const puro::OrthoParams& p, int64_t p
 }
 
 // One cluster's shared memory and registers hold it: up to 128 on a side.
-// (128 x 128: 31 us against 93 by the general kernel, 100 x 1800: 60 against 118.)
+// (128 x 128: 33 us against 54 by the general kernel, 100 x 1800: 59 against 84.)
 bool ortho_small(int64_t n, int64_t k) {
   return std::min(n, k) <= puro::kSmallSide && std::max(n, k) <= puro::kSmallSlice * puro::kSmallMaxCluster;
 }
