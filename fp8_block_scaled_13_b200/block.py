@@ -74,8 +74,10 @@ def residual_norm(x: torch.Tensor, w_pre: torch.Tensor, h: torch.Tensor | None =
     """y = x + scale * gate * post(h), then n = y / rms(y) * w_pre, the input of the next linear.
 
     x, h [rows, cols] BF16; post is the RMS norm with weight w_post, or nothing.  Without h, y is x and only the
-    norm is taken.  gate is [rows, 1], [1, cols] or [rows, cols].  The stored (BF16) y is what the norm sees.
-    `y` may be x itself (the sum is then taken in place)."""
+    norm is taken.  gate is [rows, 1], [1, cols] or [rows, cols] (with one row, [1, cols] is a gate per channel).  The
+    stored (BF16) y is what the norm sees; it equals x.float() + scale * ((hh * w_post) * gate) in separate FP32
+    operations, rounded.  `y` may be x or h itself (the sum is then taken in place); results must not overlap inputs
+    or one another otherwise."""
     flag = _layout_flag(layout)
     r = (_native or _load()).residual_norm(x, w_pre, h, w_post, gate, scale, eps, flag, y, out)
     if r[0]:
@@ -96,7 +98,7 @@ def residual_norm_backward(dn: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor
     y, rstd, rstd_post: what residual_norm returned; h, the weights, gate and scale: what it was given.  dh comes
     back in `layout`, as the dY of the linear that made h.  dw_pre, dw_post and dgate may be given; with
     accumulate=True the weights' gradients, and the gradient of a gate [1, cols], are added into the given FP32
-    buffers."""
+    buffers.  `dx` may be dn, y or dy itself; results must not overlap inputs or one another otherwise."""
     flag = _layout_flag(layout)
     r = (_native or _load()).residual_norm_backward(dn, y, rstd, w_pre, h, dy, w_post, rstd_post, gate, scale, flag, dx,
                                                     out, dw_pre, dw_post, dgate, accumulate)
@@ -111,7 +113,7 @@ def residual_norm_backward(dn: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor
 
 def swiglu(gu: torch.Tensor, layout: str = "both", out: QuantAct | torch.Tensor | None = None):
     """silu(g) * u of gu = [g | u] [rows, 2f] BF16, the fused gate+up projection's output, as the QuantAct (or, with
-    layout="bf16", the BF16 tensor) that the down projection takes."""
+    layout="bf16", the BF16 tensor) that the down projection takes.  `out` must not overlap gu."""
     flag = _layout_flag(layout)
     r = (_native or _load()).swiglu(gu, flag, out)
     if r[0]:
@@ -122,7 +124,7 @@ def swiglu(gu: torch.Tensor, layout: str = "both", out: QuantAct | torch.Tensor 
 def swiglu_backward(da: torch.Tensor, gu: torch.Tensor, layout: str = "both",
                     out: QuantAct | torch.Tensor | None = None):
     """[dg | du] of swiglu from da [rows, f] BF16, as the dY of the gate+up projection (QuantAct, or BF16 with
-    layout="bf16")."""
+    layout="bf16").  `out` must not overlap da or gu."""
     flag = _layout_flag(layout)
     r = (_native or _load()).swiglu_backward(da, gu, flag, out)
     if r[0]:

@@ -205,7 +205,7 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 // ones are worked on.  A thread reads only what it copied itself, so the copies
 // need no barrier, and 80 KB per CTA stay in flight.  (A forward pass with a
 // warp to a row, loading into registers, kept the memory busy for two thirds
-// of the time: 84 us for 32768 x 2048 against 77.)
+// of the time: 84 us for 32768 x 2048 against 76.)
 
 constexpr uint32_t kNormRedBytes = 2 * 32 * 8 * 4;
 
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : MAXT == 512 ? 2 : 1) n
           for (int i = 0; i < 4; ++i) h[i] = mul2(h[i], g[i]);
         }
         // (a product with one, or with a power of two, is exact, so that the fused
-        // form rounds as an addition does)
+        // form rounds as an addition does; a plain packed sum the compiler would fuse
+        // with the product before it, in spite of the roundings that both name)
         if (!p.scale_pow2) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = mul2(h[i], f2_both(p.scale));

@@ -271,13 +271,6 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// A sum that stays apart from a product before it.  (The compiler fuses
-// add.rn.f32x2 with mul.rn.f32x2 in spite of their roundings; scalar adds it does
-// not: 768673 of 4 M sums x + 0.3 h came out fused, 0 so.)
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  const float2 x = f2_get(a), y = f2_get(b);
-  return f2_of(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
-}
 __device__ __forceinline__ f2 f2_both(float v) { return f2_of(v, v); }
 __device__ __forceinline__ float f2_sum(f2 v) {
   const float2 p = f2_get(v);

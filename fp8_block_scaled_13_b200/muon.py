@@ -21,7 +21,9 @@ def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7
     odd quintic a x + b x^3 + c x^5 reach from g / (|g| + eps), as BF16 [n, k].
 
     The coefficients must keep singular values that start in [0, 1] below 2, as Muon's do.  |g| is summed in FP32: it
-    has to stay below 1e18, and eps should be small beside it (a g / eps below 1e-4 loses digits).
+    has to stay between 1e-18 and 1e18, and eps should be small beside it (a g / eps below 1e-4 loses digits).  The same
+    g gives the same result.  A large g takes a cooperative launch, which waits until it fits on the device beside what
+    runs on other streams.
     `workspace`: a contiguous CUDA uint8 tensor of at least orthogonalize_workspace_bytes(n, k) bytes, on a 256-byte
     boundary (as torch allocates), to use instead of allocating it; calls that may run at the same time need distinct
     ones.  Neither it nor `out` may overlap another of the call's tensors."""

@@ -391,8 +391,8 @@ PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
  *   X0 = G / (|G|_F + eps);  steps times X <- a X + (b M + c M^2) X, M = X X^T
  * (for n > k on the other side: M = X^T X, X <- a X + X (b M + c M^2)).
  * g    : [n, k] FP32 (g_f32 = 1, e.g. a main gradient) or BF16 (0), any row
- *        stride ld_g >= k and any alignment of its type; |g| below 1e18 (its
- *        squares are summed in FP32).
+ *        stride ld_g >= k and any alignment of its type; |g| between 1e-18 and
+ *        1e18 (its squares are summed in FP32).
  * out  : BF16 [n, k], any row stride ld_out >= k; must not overlap g, and the
  *        workspace neither of them.
  * X is held to 22 significant bits (two FP16 terms), the diagonals of M and of
