@@ -93,3 +93,16 @@ def test_ten_steps_of_what_lacks_directions(fp8, n, k):
         if name in ("rank 1", "rank 4"):
             off = _off(fp8.orthogonalize(g, steps=10), _reference(g, 10))
             assert off <= bound, (name, off)
+
+
+@pytest.mark.parametrize("n,k", [(1, 5000), (5000, 1), (2, 65536), (65536, 3), (128, 2049), (2049, 128), (33, 10000),
+                                 (10000, 31), (127, 4097)])
+def test_far_from_square(fp8, n, k):
+    """Beyond the sides of the small kernel by one of them only: products of few rows over long sums.  Few rows average
+    less: a rounding of O or R, a step of 2^-10 at most, may count whole, 2 in each of 5 steps and what they leave, and the
+    bound is that of few values."""
+    for name, g, _ in _gradients(n, k):
+        want = _reference(g)
+        off = _off(fp8.orthogonalize(g), want)
+        assert off <= HALF + 10 * 2.0 ** -10, (name, off)
+    assert fp8.device_status() == 0
