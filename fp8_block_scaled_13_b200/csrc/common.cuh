@@ -14,7 +14,8 @@ constexpr int kOk = 0;
 constexpr int kErrDeviceTimeout = -7;
 
 // Default limit of every on-device wait, in nanoseconds.  No legitimate wait
-// in these kernels lasts more than a few microseconds.
+// in these kernels lasts more than a few microseconds, but for the one between two
+// products of an orthogonalisation: a tile's time, below a millisecond.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // The device error word: 0, or the first error a kernel recorded.  Read and
