@@ -35,8 +35,8 @@
 // direction that G lacks up by a, to 2e-2 to 7e-2 in ten steps.  (Two BF16 terms
 // per operand and three products each took twice as long: 2168 us against 1133
 // for 12288 x 2048.)  A short sum averages less, so X X^T over up to kOrthoExactK
-// takes three products, hi hi + hi lo + lo hi, where launches and not products are
-// the time anyway.
+// takes three products, hi hi + hi lo + lo hi, and R X of up to kOrthoFewRows rows
+// two, R hi + R lo, where launches and not products are the time anyway.
 // Powers of two keep FP16 in range: X is stored times 2^10, M times 2^13, R
 // times 2^12, which holds while |X| < 64, |M| < 8 and |R| < 16 off the
 // diagonal; the iteration keeps singular values near 1.
@@ -80,6 +80,7 @@ enum OrthoProduct : int { kOrthoGram = 0, kOrthoPoly = 1, kOrthoUpdate = 2 };
 
 constexpr int kOrthoNormBlocks = 592;  // most CTAs of the passes over G, one partial sum each
 constexpr int64_t kOrthoExactK = 1024; // longest X X^T sum that takes three products
+constexpr int64_t kOrthoFewRows = 128; // longest R X sum that takes two
 constexpr int kOrthoLate = 2;           // last steps in which all of X meets the diagonal of R
 constexpr float kXScale = 1024.f, kMScale = 8192.f, kRScale = 4096.f;
 constexpr int kOrthoMaxSplit = 8;
@@ -89,7 +90,7 @@ constexpr int kOrthoMaxSplit = 8;
 struct OrthoShape {
   int32_t rows_a, rows_b;   // D is [rows_a, rows_b]
   int32_t kblocks;          // ceil(K / 64)
-  int32_t passes;           // 1: hi hi; 3: hi hi, hi lo, lo hi
+  int32_t passes;           // 1: hi hi; 3: hi hi, hi lo, lo hi; the update's 2: R hi, R lo
   int32_t bn;               // columns of a tile: 256, 128 or 64 (its rows are 256)
   int32_t tiles_m, tiles_n;
   int32_t full, split, units;
@@ -118,7 +119,7 @@ constexpr int kOrthoCounters = 64 + 3 * kSplitTiles * 2;
 // 32 x 32 with the 64-byte swizzle.
 struct OrthoMaps {
   CUtensorMap gram[2][2], gram_b[2][2];  // X as the operands of X X^T: [buffer][hi, lo]
-  CUtensorMap update[2];                 // X hi as an operand of the update
+  CUtensorMap update[2][2];              // X as an operand of the update: [buffer][hi, lo]
   CUtensorMap o, o_b;                    // O, both operands of the square
   CUtensorMap r;                         // R, an operand of the update
   CUtensorMap ex[2][2], eo, er, out;
@@ -312,6 +313,7 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
                                            int cluster_id, int clusters, uint32_t rank, uint32_t& blocks,
                                            const Barrier& arrived) {
   using C = OrthoCfg;
+  constexpr int32_t kLoA = SYM ? 2 : 1;  // the pass that takes A's lo term (of R there is none)
   // both CTAs' bytes of a stage
   const uint32_t bytes = 2 * (C::kTile + (BMN ? (s.bn == 256 ? 16384u : 8192u) : (uint32_t)s.bn * 64));
   const uint32_t full = smem_u32(sm.full), empty = smem_u32(sm.empty), base = smem_u32(sm.base);
@@ -325,7 +327,7 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
       const int32_t a0 = t.y0 + 128 * (int32_t)rank;
       const int32_t b0 = t.x0 + (t.cols >> 1) * (int32_t)rank;
       int32_t pass = s.passes == 1 || t.k0 == 0 ? 0 : t.k0 / s.kblocks, k = (t.k0 - pass * s.kblocks) * 64;
-      const CUtensorMap* ma = pass == 2 ? al : ah;
+      const CUtensorMap* ma = pass == kLoA ? al : ah;
       const CUtensorMap* mb = pass == 1 ? bl : bh;
       for (int32_t n = t.k1 - t.k0; n > 0; --n) {
         const uint32_t stage = blocks % C::kStages, odd = blocks / C::kStages & 1, at = full + stage * 8;
@@ -348,10 +350,10 @@ __device__ __forceinline__ bool ortho_load(const OrthoSmem& sm, const OrthoShape
           ortho_tma(db, mb, k, b0, bar);
         }
         k += 64;
-        if (SYM && k >= k_end) {
+        if (k >= k_end) {
           k = 0;
           ++pass;
-          ma = pass == 2 ? al : ah;
+          ma = pass == kLoA ? al : ah;
           mb = pass == 1 ? bl : bh;
         }
       }
@@ -483,8 +485,9 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoSmem& sm, const OrthoP
     float raw_scale = p.c / (kMScale * kMScale), c_r = p.c * (kRScale / kMScale);
     float base_r = EPI == kOrthoPoly ? fmaf(p.c, dr, p.b) * (kRScale / kMScale) : p.a + dr;
     float d_own = dr * fmaf(p.c, dr, p.b);
-    // the update's factors of X's terms: a + D' for hi, for lo a, and a + D' late
-    const float late = step + kOrthoLate >= p.steps ? 1.f : 0.f, k_low = fmaf(late, dr, p.a);
+    // the update's factors of X's terms: a + D' for hi, for lo a, and a + D' late or
+    // where R meets lo too
+    const float late = s.passes == 2 || step + kOrthoLate >= p.steps ? 1.f : 0.f, k_low = fmaf(late, dr, p.a);
     if (EPI != kOrthoGram) asm volatile("" : "+f"(raw_scale), "+f"(c_r), "+f"(base_r), "+f"(d_own));
     if (!mbar_wait_warp(&sm.accf[acc], (st.it >> 1) & 1, sm.abort_flag)) return false;
     tc_fence_after();
@@ -789,10 +792,10 @@ __global__ void __launch_bounds__(OrthoCfg::kThreads, 1)
         ok = ortho_load<true, false, false>(sm, p.shape[kOrthoPoly], &m.o, &m.o, &m.o_b, &m.o_b, cluster_id, clusters,
                                             rank, blocks, arrived);
       else if (TALL)
-        ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur], &m.update[cur], &m.r, &m.r,
+        ok = ortho_load<false, false, false>(sm, p.shape[kOrthoUpdate], &m.update[cur][0], &m.update[cur][1], &m.r, &m.r,
                                              cluster_id, clusters, rank, blocks, arrived);
       else
-        ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur], &m.update[cur],
+        ok = ortho_load<false, false, true>(sm, p.shape[kOrthoUpdate], &m.r, &m.r, &m.update[cur][0], &m.update[cur][1],
                                             cluster_id, clusters, rank, blocks, arrived);
       if (!ok && !p.one_cluster) break;
     }

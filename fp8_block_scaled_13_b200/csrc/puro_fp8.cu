@@ -1277,7 +1277,7 @@ OrthoPlan ortho_plan_for(int64_t n, int64_t k, int64_t pairs) {
     s.rows_a = (int32_t)rows[i];
     s.rows_b = (int32_t)cols[i];
     s.kblocks = (int32_t)((sums[i] + 63) / 64);
-    s.passes = i == puro::kOrthoGram && w <= puro::kOrthoExactK ? 3 : 1;
+    s.passes = i == puro::kOrthoGram && w <= puro::kOrthoExactK ? 3 : i == puro::kOrthoUpdate && m <= puro::kOrthoFewRows ? 2 : 1;
     const int64_t tm = (rows[i] + 255) / 256, total = (int64_t)s.kblocks * s.passes;
     int64_t best = INT64_MAX;
     for (int j = 0; j < 3; ++j) {
@@ -1561,11 +1561,11 @@ extern "C" int puro_fp8_orthogonalize(const void* g, int64_t ld_g, int g_f32, in
   for (int i = 0; i < 2; ++i) {
     for (int t = 0; t < 2; ++t) {
       if ((st = make_map_16(&maps.gram[i][t], at(l.x[i][t]), k, n, l.ld_x, 64, tall ? 64 : 128, sw)) != PURO_OK ||
+          (st = make_map_16(&maps.update[i][t], at(l.x[i][t]), k, n, l.ld_x, 64, tall ? 128 : 64, sw)) != PURO_OK ||
           (st = make_map_16(&maps.gram_b[i][t], at(l.x[i][t]), k, n, l.ld_x, 64, tall ? 64 : half(0), sw)) != PURO_OK ||
           (st = make_map_16(&maps.ex[i][t], at(l.x[i][t]), k, n, l.ld_x, 32, 32, sw_e)) != PURO_OK)
         return st;
     }
-    if ((st = make_map_16(&maps.update[i], at(l.x[i][0]), k, n, l.ld_x, 64, tall ? 128 : 64, sw)) != PURO_OK) return st;
   }
   if ((st = make_map_16(&maps.o, at(l.o), m, m, l.ld_m, 64, 128, sw)) != PURO_OK ||
       (st = make_map_16(&maps.o_b, at(l.o), m, m, l.ld_m, 64, half(1), sw)) != PURO_OK ||

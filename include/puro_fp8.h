@@ -400,7 +400,7 @@ PURO_API int64_t puro_fp8_orthogonalize_workspace_bytes(int64_t n, int64_t k);
  * product is rounded to FP16 off the diagonal, up or down at random by bits that
  * follow from its place (results repeat), and out to BF16 once.  In 5 steps that
  * adds 0.3e-3 to 1.1e-3 of the result to the rounding of out where the shorter
- * side is above 128, up to 1.8e-3 where there are few rows; every further step
+ * side is above 128, up to 1.6e-3 where there are few rows; every further step
  * lifts by a what 22 bits leave in directions that G lacks.
  * 1 <= n, k <= 65536 (0: no-op); 1 <= steps <= 64; eps >= 0; coefficients that
  * let a singular value from [0, 1] reach 2 are refused (PURO_ERR_SHAPE).
