@@ -1249,7 +1249,7 @@ constexpr int64_t kOrthoMaxDim = 65536;
 // epilogue, which two sets of warps share; a split tile's hand-over, and writing
 // and reading 32 columns of partials.  (200 x 333: 74 us against 118 with 256
 // columns throughout, 512 x 512: 97 against 146, 2048 x 2048: 219 against 239,
-// and 327 with 64 throughout; without splits 900 x 900 takes 142 against 131.)
+// and 327 with 64 throughout; without splits 900 x 900 takes 142 against 133.)
 constexpr int64_t kOrthoPairs = kSms / 2;
 constexpr int64_t kOrthoBlockCycles[3] = {510, 380, 280};  // 256, 128, 64 columns
 constexpr int64_t kOrthoChunkCycles = 1500;
@@ -1331,7 +1331,7 @@ OrthoPlan ortho_plan(int64_t n, int64_t k) {
 
 // Where the workspace of an n x k problem keeps its matrices, in bytes, each
 // from a multiple of 256 on.  Rows start on multiples of 128 bytes: the 128-byte
-// rows that TMA reads would else each touch two lines of L2 (900 x 900: 131 us
+// rows that TMA reads would else each touch two lines of L2 (900 x 900: 133 us
 // against 155).
 struct OrthoLayout {
   int64_t ld_x, ld_m;
